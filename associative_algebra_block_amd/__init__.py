@@ -22,7 +22,9 @@ __all__ = [
     "aa_plan_create", "aa_plan_create_digraph", "aa_plan_destroy", "aa_plan_info", "aa_packed_layout_version",
     "aa_pack_weights", "aa_unpack_weights",
     "aa_project_fwd", "aa_swiglu_ffn_fwd", "aa_swiglu_ffn_fwd_noalloc", "aa_decode_gemv", "aa_project_bwd_workspace",
-    "aa_project_bwd_data", "aa_project_bwd_weight", "aa_set_kernel_events", "aa_status_string", "aa_last_error",
+    "aa_project_bwd_data", "aa_project_bwd_weight",
+    "aa_layernorm_fwd", "aa_layernorm_bwd", "aa_layernorm_bwd_workspace",
+    "aa_kv_append", "aa_attn_decode", "aa_attn_decode_workspace", "aa_set_kernel_events", "aa_status_string", "aa_last_error",
 ]
 
 AA_LAW_QQ, AA_LAW_Q2XQ2, AA_LAW_DIGRAPH = 0, 1, 2
@@ -65,6 +67,17 @@ _SIGNATURES = {
                                            _c_p]),
     "aa_project_bwd_weight": (ctypes.c_int, [_c_p, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_p, _c_p, ctypes.c_size_t,
                                              _c_p]),
+    "aa_layernorm_fwd": (ctypes.c_int, [_c_p] * 8 + [_c_i64, _c_i64, ctypes.c_float] + [ctypes.c_int] * 3 + [_c_p]),
+    "aa_layernorm_bwd_workspace": (ctypes.c_int, [_c_i64, _c_i64, ctypes.POINTER(ctypes.c_size_t)]),
+    "aa_layernorm_bwd": (ctypes.c_int, [_c_p] * 9 + [_c_i64, _c_i64, ctypes.c_int, ctypes.c_int, _c_p,
+                                                     ctypes.c_size_t, _c_p]),
+    "aa_kv_append": (ctypes.c_int, [_c_p, _c_p, _c_i64, _c_i64, ctypes.c_int, _c_p, _c_p, _c_i64, _c_i32, _c_i32,
+                                    _c_i32, _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_i64, _c_p]),
+    "aa_attn_decode_workspace": (ctypes.c_int, [_c_i64, _c_i32, _c_i32, _c_i32, _c_i32, _c_i64,
+                                                ctypes.POINTER(ctypes.c_size_t)]),
+    "aa_attn_decode": (ctypes.c_int, [_c_p, _c_i64, ctypes.c_int, _c_p, _c_p, _c_i64, _c_i32, _c_i32, _c_i32, _c_i32,
+                                      _c_p, _c_i64, _c_i64, _c_p, ctypes.c_float, _c_p, ctypes.c_int, _c_p,
+                                      ctypes.c_size_t, _c_p]),
     "aa_set_kernel_events": (ctypes.c_int, [_c_p, _c_p]),
     "aa_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "aa_last_error": (ctypes.c_char_p, []),
@@ -316,6 +329,176 @@ def aa_project_bwd_weight(plan: Plan, X, dY, dW_packed, M=None, pos_offset=0, ro
         _ptr(dW_packed, "dW_packed", plan.out_torch_dtype, plan.d_in * plan.d_out), M, int(pos_offset),
         _ptr(row_types, "row_types", torch.int32, M), _ptr(workspace, "workspace"), int(workspace_bytes),
         _stream(stream)), "aa_project_bwd_weight")
+
+
+def _tensor(t, name, shape, dtypes, device):
+    """Device pointer of a dense tensor of the given shape and one of the
+    given dtypes on the given device (None passed through).  The operators
+    below take tensors only: their sizes and types come from them."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _call_device(t, name):
+    """The device of a call's first operand, which must be the current one:
+    the launch goes to a stream of the current device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name}: must be a device tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, but the current device is {torch.cuda.current_device()}")
+    return t.device
+
+
+def _workspace(workspace, device):
+    """(pointer, bytes) of a workspace tensor or None."""
+    if workspace is None:
+        return None, 0
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace: expected a tensor")
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: must be contiguous and on {device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+_FLOATS = (torch.bfloat16, torch.float32)
+_F32 = (torch.float32,)
+
+
+def aa_layernorm_fwd(X, gamma, beta, Y, delta=None, S=None, mean=None, rstd=None, eps=1e-5, stream=None):
+    """Y = layernorm(X [+ delta]) over the last dimension of the M x d tensor
+    X; with delta the sum goes to S (which may be X).  gamma and beta may be
+    None; mean and rstd (M float32 values each) are for the backward pass."""
+    dev = _call_device(X, "X")
+    if X.dim() != 2:
+        raise ValueError("X: expected two dimensions")
+    shape = tuple(X.shape)
+    M, d = shape
+    _check(load().aa_layernorm_fwd(
+        _tensor(X, "X", shape, _FLOATS, dev), _tensor(delta, "delta", shape, _FLOATS, dev),
+        _tensor(gamma, "gamma", (d,), _F32, dev), _tensor(beta, "beta", (d,), _F32, dev),
+        _tensor(S, "S", shape, (X.dtype,), dev), _tensor(Y, "Y", shape, _FLOATS, dev),
+        _tensor(mean, "mean", (M,), _F32, dev), _tensor(rstd, "rstd", (M,), _F32, dev), M, d, eps,
+        _DTYPES[X.dtype], AA_F32 if delta is None else _DTYPES[delta.dtype], _DTYPES[Y.dtype], _stream(stream)),
+        "aa_layernorm_fwd")
+
+
+def aa_layernorm_bwd_workspace(M: int, d: int) -> int:
+    """Bytes of workspace that aa_layernorm_bwd needs for dgamma and dbeta."""
+    n = ctypes.c_size_t(0)
+    _check(load().aa_layernorm_bwd_workspace(int(M), int(d), ctypes.byref(n)), "aa_layernorm_bwd_workspace")
+    return int(n.value)
+
+
+def aa_layernorm_bwd(X, dY, gamma, mean, rstd, dX, dgamma=None, dbeta=None, dS=None, workspace=None, stream=None):
+    """Gradients of aa_layernorm_fwd: X is the normalised tensor (S where the
+    forward call had delta), dS the residual path's gradient (may be dX)."""
+    dev = _call_device(X, "X")
+    if X.dim() != 2:
+        raise ValueError("X: expected two dimensions")
+    shape = tuple(X.shape)
+    M, d = shape
+    xt = (X.dtype,)
+    ws, nbytes = _workspace(workspace, dev)
+    _check(load().aa_layernorm_bwd(
+        _tensor(X, "X", shape, _FLOATS, dev), _tensor(dY, "dY", shape, _FLOATS, dev),
+        _tensor(gamma, "gamma", (d,), _F32, dev), _tensor(mean, "mean", (M,), _F32, dev),
+        _tensor(rstd, "rstd", (M,), _F32, dev), _tensor(dS, "dS", shape, xt, dev), _tensor(dX, "dX", shape, xt, dev),
+        _tensor(dgamma, "dgamma", (d,), _F32, dev), _tensor(dbeta, "dbeta", (d,), _F32, dev), M, d,
+        _DTYPES[X.dtype], _DTYPES[dY.dtype], ws, nbytes, _stream(stream)), "aa_layernorm_bwd")
+
+
+_I32 = (torch.int32,)
+_BF16 = (torch.bfloat16,)
+
+
+def _token_rows(t, name, n, heads, dim, dtypes, device):
+    """(pointer, row stride) of n rows of heads x dim values, [n, heads * dim]
+    or [n, heads, dim]; a row is dense, the rows may lie further apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    shape, width = tuple(t.shape), heads * dim
+    if shape != (n, width) and shape != (n, heads, dim):
+        raise ValueError(f"{name}: shape {shape}, expected {(n, width)} or {(n, heads, dim)}")
+    if t.numel() and (t.stride(-1) != 1 and shape[-1] > 1 or t.dim() == 3 and heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name}: the values of a token must be contiguous")
+    return t.data_ptr(), t.stride(0) if n > 1 else width
+
+
+def _cache_sizes(k_pages, v_pages, page_table):
+    """(n_pages, n_kv_heads, page_size, head_dim, n_seqs, max_pages)."""
+    for t, name, dim in ((k_pages, "k_pages", 4), (v_pages, "v_pages", 4), (page_table, "page_table", 2)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a tensor")
+        if t.dim() != dim:
+            raise ValueError(f"{name}: {t.dim()} dimensions, expected {dim}")
+    n_pages, hkv, page, dim = k_pages.shape
+    return n_pages, hkv, page, dim, page_table.shape[0], page_table.shape[1]
+
+
+def aa_kv_append(K, V, k_pages, v_pages, page_table, pos, seq=None, stream=None):
+    """Write the keys and values of n tokens ([n, kv heads * head dim] or
+    [n, kv heads, head dim], rows of any stride) to their places in the cache:
+    token t to position pos[t] of sequence seq[t] (None: sequence t)."""
+    dev = _call_device(k_pages, "k_pages")
+    n_pages, hkv, page, dim, n_seqs, max_pages = _cache_sizes(k_pages, v_pages, page_table)
+    if not isinstance(pos, torch.Tensor) or pos.dim() != 1:
+        raise ValueError("pos: expected a tensor of one dimension")
+    n = pos.shape[0]
+    k, ldk = _token_rows(K, "K", n, hkv, dim, _FLOATS, dev)
+    v, ldv = _token_rows(V, "V", n, hkv, dim, (K.dtype,), dev)
+    _check(load().aa_kv_append(
+        k, v, ldk, ldv, _DTYPES[K.dtype],
+        _tensor(k_pages, "k_pages", (n_pages, hkv, page, dim), _BF16, dev),
+        _tensor(v_pages, "v_pages", (n_pages, hkv, dim, page), _BF16, dev), n_pages, page, hkv, dim,
+        _tensor(page_table, "page_table", (n_seqs, max_pages), _I32, dev), n_seqs, max_pages,
+        _tensor(seq, "seq", (n,), _I32, dev), _tensor(pos, "pos", (n,), _I32, dev), n, _stream(stream)),
+        "aa_kv_append")
+
+
+def aa_attn_decode_workspace(n_seqs, n_heads, n_kv_heads, head_dim, page_size, max_pages) -> int:
+    """Bytes of workspace that aa_attn_decode needs."""
+    n = ctypes.c_size_t(0)
+    _check(load().aa_attn_decode_workspace(int(n_seqs), int(n_heads), int(n_kv_heads), int(head_dim), int(page_size),
+                                           int(max_pages), ctypes.byref(n)), "aa_attn_decode_workspace")
+    return int(n.value)
+
+
+def aa_attn_decode(Q, k_pages, v_pages, page_table, lengths, O, scale, workspace=None, stream=None):
+    """O [n_seqs, heads, head dim] = attention of the queries Q ([n_seqs,
+    heads * head dim] or [n_seqs, heads, head dim], rows of any stride) over
+    the first lengths[s] positions of each sequence."""
+    dev = _call_device(k_pages, "k_pages")
+    n_pages, hkv, page, dim, n_seqs, max_pages = _cache_sizes(k_pages, v_pages, page_table)
+    if not isinstance(O, torch.Tensor) or O.dim() != 3:
+        raise ValueError("O: expected a tensor of three dimensions")
+    heads = O.shape[1]
+    q, ldq = _token_rows(Q, "Q", n_seqs, heads, dim, _FLOATS, dev)
+    ws, nbytes = _workspace(workspace, dev)
+    _check(load().aa_attn_decode(
+        q, ldq, _DTYPES[Q.dtype],
+        _tensor(k_pages, "k_pages", (n_pages, hkv, page, dim), _BF16, dev),
+        _tensor(v_pages, "v_pages", (n_pages, hkv, dim, page), _BF16, dev), n_pages, page, heads, hkv, dim,
+        _tensor(page_table, "page_table", (n_seqs, max_pages), _I32, dev), n_seqs, max_pages,
+        _tensor(lengths, "lengths", (n_seqs,), _I32, dev), scale,
+        _tensor(O, "O", (n_seqs, heads, dim), _FLOATS, dev), _DTYPES[O.dtype], ws, nbytes, _stream(stream)),
+        "aa_attn_decode")
 
 
 def _event(ev):

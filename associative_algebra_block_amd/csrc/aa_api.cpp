@@ -5,26 +5,15 @@
 
 #include <string>
 
+#include "aa_checks.h"
 #include "aa_internal.h"
 
+using aa::check_ptr;
+using aa::elem_size;
 using aa::fail;
+using aa::overlaps;
 
 namespace {
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-aa_status_t check_ptr(const void* p, const char* what, const char* fn) {
-  if (!p) return fail(AA_ERR_INVALID_ARG, std::string(fn) + ": " + what + " is NULL");
-  if (!aligned16(p)) return fail(AA_ERR_INVALID_ARG, std::string(fn) + ": " + what + " is not 16-byte aligned");
-  return AA_OK;
-}
-
-size_t elem_size(aa_dtype_t t) { return t == AA_F32 ? 4 : 2; }
-
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
-}
 
 // Checks shared by the row-typed calls: M, the position offset and the type map.
 aa_status_t check_rows(const aa_plan_s& plan, int64_t M, int64_t pos_offset, const int32_t* row_types,

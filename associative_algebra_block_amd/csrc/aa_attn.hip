@@ -1,0 +1,430 @@
+// Attention of one new token per sequence over a paged key-value cache, and
+// the append that writes new tokens into the cache.
+//
+//   s_j = scale q . k_j  (0 <= j < length),  p = softmax(s),  o = sum_j p_j v_j
+//
+// The cache is bf16: pages of `page` positions (a power of two), keys as
+// [page id][kv head][position][feature], values as [page id][kv head][feature]
+// [position].  With the values transposed, both products read their cache
+// operand straight into matrix fragments, 16 bytes a lane, and nothing of the
+// cache passes through LDS:
+//   S^T (keys x heads)  = K (16 keys x 32 features) . Q^T
+//   O^T (features x heads) += V^T (16 features x 32 keys) . P^T
+// The key order inside a product is free, so the 32 keys of a step are dealt
+// to the two S^T fragments such that the lane that holds a probability is the
+// lane that needs it for the second product: lane (head n, group g) gets keys
+// 8 g + 4 t + i in element i of fragment t, and feeds keys 8 g .. 8 g + 7.
+//
+// The cache crosses HBM once and that bounds the call: 4 G operations a loaded
+// byte pair (G query heads share a kv head) are far below the matrix rate even
+// where only one of a fragment's 16 head columns is in use.  The matrix slack
+// pays for exactness: float32 queries go in as three bf16 terms, the
+// probabilities as two (three for float32 outputs), so neither is rounded to
+// bf16.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "aa_device.h"
+#include "aa_internal.h"
+
+namespace aa {
+namespace {
+
+constexpr int kKeys = 32;        // keys of one step of a wave
+constexpr int kAttnWaves = 4;
+constexpr int kMinTiles = 8;     // steps of a workgroup below which a sequence is not split further
+constexpr int kMaxSplit = 256;
+constexpr float kLog2e = 1.4426950408889634f;
+
+typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
+typedef __bf16 bf16x8_u __attribute__((ext_vector_type(8), aligned(2)));
+
+struct AttnParams {
+  const void* Q;
+  const __bf16* K;
+  const __bf16* V;
+  const int32_t* table;
+  const int32_t* lens;
+  void* O;
+  float* part;       // [B H][nsplit][D], unnormalised
+  float* ml;         // [B H][nsplit][2]: running maximum (log2 scale) and sum
+  int64_t ldq, n_pages, max_pages;
+  int32_t B, H, Hkv, G, D, head_tiles, page_shift, nsplit, o_f32;
+  float scale;
+};
+
+// The tiles of a sequence that split s of nsplit takes.
+struct TileRange {
+  int64_t begin, end;
+};
+__device__ inline TileRange split_tiles(int64_t len, int nsplit, int s, int* used) {
+  const int64_t tiles = (len + kKeys - 1) / kKeys;
+  const int64_t per = max((tiles + nsplit - 1) / nsplit, int64_t(kMinTiles));
+  *used = int((tiles + per - 1) / per);
+  return {min(s * per, tiles), min((s + 1) * per, tiles)};
+}
+
+// x = hi + mid + lo exactly to 24 bits, each a bf16.
+__device__ inline void split3(float x, __bf16* t) {
+  t[0] = (__bf16)x;
+  float r = x - float(t[0]);
+  t[1] = (__bf16)r;
+  t[2] = (__bf16)(r - float(t[1]));
+}
+
+__device__ inline bf16x8_t as_frag(u32x4_t v) { return __builtin_bit_cast(bf16x8_t, v); }
+__device__ inline f32x4_t mfma(bf16x8_t a, bf16x8_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// DC: 32-wide feature chunks (D <= 32 DC).  NQ: bf16 terms of a query; NP: of
+// a probability.
+template <int DC, typename TQ, int NP>
+__global__ __launch_bounds__(kAttnWaves * 64) void attn_decode_kernel(AttnParams p) {
+  constexpr int NQ = sizeof(TQ) == 4 ? 3 : 1;
+  constexpr int DT = 2 * DC;             // 16-wide feature tiles of the output
+  constexpr int kRow = 16 * DT + 4;      // floats of one head's row in LDS
+  __shared__ float s_acc[kAttnWaves][16][kRow];
+  __shared__ float s_ml[kAttnWaves][16][2];
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int n = lane & 15, g = lane >> 4;
+  int64_t w = blockIdx.x;
+  const int split = int(w % p.nsplit);
+  w /= p.nsplit;
+  const int ht = int(w % p.head_tiles);
+  w /= p.head_tiles;
+  const int hkv = int(w % p.Hkv);
+  const int b = int(w / p.Hkv);
+  const int heads = min(16, p.G - 16 * ht);              // query heads of this workgroup
+  const int head0 = hkv * p.G + 16 * ht;
+
+  int64_t len = p.lens[b];
+  bool bad = len < 0 || len > (p.max_pages << p.page_shift);
+  if (bad) len = 0;
+  int used;
+  const TileRange r = split_tiles(len, p.nsplit, split, &used);
+  if (split >= max(used, 1)) return;
+
+  // queries: lane n holds features 32 c + 8 g .. + 7 of head n
+  bf16x8_t q[NQ][DC];
+#pragma unroll
+  for (int c = 0; c < DC; ++c) {
+    float x[8];
+    const int f = 32 * c + 8 * g;
+    const bool ok = n < heads && f < p.D;
+    const TQ* src = static_cast<const TQ*>(p.Q) + b * p.ldq + int64_t(head0 + n) * p.D + f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = ok ? float(src[e]) : 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      __bf16 t[3];
+      split3(x[e], t);
+#pragma unroll
+      for (int k = 0; k < NQ; ++k) q[k][c][e] = t[k];
+    }
+  }
+
+  f32x4_t acc[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d) acc[d] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  float m = -INFINITY, l = 0.0f;
+  const float c2 = p.scale * kLog2e;
+  const int64_t last = len - 1;
+  const int64_t page_elems = int64_t(p.D) << p.page_shift;   // of one head's page
+  const int64_t page_mask = (int64_t(1) << p.page_shift) - 1;
+  const int32_t* row = p.table + b * p.max_pages;
+
+  for (int64_t tile = r.begin + wave; tile < r.end; tile += kAttnWaves) {
+    // positions behind the end read the last one's place: their scores are
+    // masked and their values zeroed below
+    const int64_t kkey = tile * kKeys + 8 * (n >> 2);           // the key fragments' group of 8
+    const int64_t vkey = min(tile * kKeys + 8 * g, last & ~int64_t(7));
+    int64_t kpage = row[min(kkey, last) >> p.page_shift], vpage = row[vkey >> p.page_shift];
+    const bool wrong = kpage < 0 || kpage >= p.n_pages || vpage < 0 || vpage >= p.n_pages;
+    if (wrong) kpage = vpage = 0;
+    bad |= wrong;
+    const __bf16* kbase = p.K + (kpage * p.Hkv + hkv) * page_elems;
+    const __bf16* vbase = p.V + (vpage * p.Hkv + hkv) * page_elems + (vkey & page_mask);
+    u32x4_t kf[2][DC], vf[DT];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const __bf16* src = kbase + (min(kkey + 4 * t + (n & 3), last) & page_mask) * p.D;
+#pragma unroll
+      for (int c = 0; c < DC; ++c) {
+        const int f = 32 * c + 8 * g;
+        kf[t][c] = *reinterpret_cast<const u32x4_t*>(src + (f < p.D ? f : 0));
+      }
+    }
+#pragma unroll
+    for (int d = 0; d < DT; ++d) {
+      const int f = min(16 * d + n, p.D - 1);
+      vf[d] = *reinterpret_cast<const u32x4_t*>(vbase + (int64_t(f) << p.page_shift));
+    }
+    // features behind D: zero (a zero query alone would turn an infinite key into a NaN)
+#pragma unroll
+    for (int c = DC - 1; c < DC; ++c)
+      if (32 * c + 8 * g >= p.D) kf[0][c] = kf[1][c] = u32x4_t{0u, 0u, 0u, 0u};
+
+    f32x4_t s[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      s[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int c = 0; c < DC; ++c) s[t] = mfma(as_frag(kf[t][c]), q[0][c], s[t]);
+      if constexpr (NQ > 1) {
+        f32x4_t lo = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = NQ - 1; k >= 1; --k)     // the smallest terms first
+#pragma unroll
+          for (int c = 0; c < DC; ++c) lo = mfma(as_frag(kf[t][c]), q[k][c], lo);
+        // an infinite key: the leading term has the query's sign, the others need not
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[t][i] = __builtin_isfinite(s[t][i]) ? s[t][i] + lo[i] : s[t][i];
+      }
+    }
+    const int64_t left = len - (tile * kKeys + 8 * g);          // positions of this lane's 8 that count
+    float mx = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[t][i] = 4 * t + i < left ? s[t][i] * c2 : -INFINITY;
+        mx = fmaxf(mx, s[t][i]);
+      }
+    mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+    mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+    const float m_new = fmaxf(m, mx);
+    const float mu = m_new == -INFINITY ? 0.0f : m_new;          // all scores -inf so far: their weights are 0
+    const float alpha = __builtin_amdgcn_exp2f(m - mu);
+    m = m_new;
+    float sum = 0.0f;
+    bf16x8_t pf[NP];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float e = __builtin_amdgcn_exp2f(s[t][i] - mu);
+        sum += e;
+        __bf16 term[3];
+        split3(e, term);
+#pragma unroll
+        for (int k = 0; k < NP; ++k) pf[k][4 * t + i] = term[k];
+      }
+    l = l * alpha + sum;
+    if (left < 8) {   // what lies behind the end may be anything, NaN included: 0 . NaN is no zero
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          vf[d][j] &= (2 * j < left ? 0xffffu : 0u) | (2 * j + 1 < left ? 0xffff0000u : 0u);
+    }
+#pragma unroll
+    for (int d = 0; d < DT; ++d) {
+      acc[d] *= alpha;
+#pragma unroll
+      for (int k = NP - 1; k >= 0; --k) acc[d] = mfma(as_frag(vf[d]), pf[k], acc[d]);
+    }
+  }
+
+  // join the waves: lane (n, g) holds features 16 d + 4 g .. + 3 of head n
+  l += __shfl_xor(l, 16, 64);
+  l += __shfl_xor(l, 32, 64);
+  if (__any(bad)) l = NAN;   // a page outside the cache: the result is no number
+  if (g == 0) {
+    s_ml[wave][n][0] = m;
+    s_ml[wave][n][1] = l;
+  }
+#pragma unroll
+  for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4_t*>(&s_acc[wave][n][16 * d + 4 * g]) = acc[d];
+  __syncthreads();
+  for (int i = threadIdx.x; i < heads * p.D; i += kAttnWaves * 64) {
+    const int hn = i / p.D, f = i - hn * p.D;
+    float mm = s_ml[0][hn][0];
+#pragma unroll
+    for (int v = 1; v < kAttnWaves; ++v) mm = fmaxf(mm, s_ml[v][hn][0]);
+    const float mu = mm == -INFINITY ? 0.0f : mm;
+    float ll = 0.0f, o = 0.0f;
+#pragma unroll
+    for (int v = 0; v < kAttnWaves; ++v) {
+      const float e = __builtin_amdgcn_exp2f(s_ml[v][hn][0] - mu);
+      ll += e * s_ml[v][hn][1];
+      o += e * s_acc[v][hn][f];
+    }
+    const int64_t out = int64_t(b) * p.H + head0 + hn;
+    if (p.nsplit == 1) {
+      o = p.lens[b] == 0 ? 0.0f : o / ll;   // no position: zeros
+      if (p.o_f32) static_cast<float*>(p.O)[out * p.D + f] = o;
+      else static_cast<__bf16*>(p.O)[out * p.D + f] = (__bf16)o;
+    } else {
+      const int64_t at = out * p.nsplit + split;
+      p.part[at * p.D + f] = o;
+      if (f == 0) {
+        p.ml[2 * at] = mm;
+        p.ml[2 * at + 1] = ll;
+      }
+    }
+  }
+}
+
+// Joins the splits of one (sequence, head): one workgroup of 64 lanes each.
+__global__ __launch_bounds__(64) void attn_join_kernel(AttnParams p) {
+  const int64_t out = blockIdx.x;
+  const int b = int(out / p.H);
+  int64_t len = p.lens[b];
+  if (len < 0 || len > (p.max_pages << p.page_shift)) len = 0;   // split 0 wrote a NaN
+  int used;
+  split_tiles(len, p.nsplit, 0, &used);
+  used = max(used, 1);
+  const float* ml = p.ml + 2 * out * p.nsplit;
+  float mm = -INFINITY;
+  for (int s = threadIdx.x; s < used; s += 64) mm = fmaxf(mm, ml[2 * s]);
+#pragma unroll
+  for (int x = 32; x >= 1; x >>= 1) mm = fmaxf(mm, __shfl_xor(mm, x, 64));
+  const float mu = mm == -INFINITY ? 0.0f : mm;
+  for (int f = threadIdx.x; f < p.D; f += 64) {
+    float ll = 0.0f, o = 0.0f;
+#pragma unroll 8
+    for (int s = 0; s < used; ++s) {
+      const float e = __builtin_amdgcn_exp2f(ml[2 * s] - mu);
+      ll += e * ml[2 * s + 1];
+      o += e * p.part[(out * p.nsplit + s) * p.D + f];
+    }
+    o = p.lens[b] == 0 ? 0.0f : o / ll;
+    if (p.o_f32) static_cast<float*>(p.O)[out * p.D + f] = o;
+    else static_cast<__bf16*>(p.O)[out * p.D + f] = (__bf16)o;
+  }
+}
+
+struct AppendParams {
+  const void* K;
+  const void* V;
+  __bf16* Kp;
+  __bf16* Vp;
+  const int32_t* table;
+  const int32_t* seq;   // or nullptr: token t belongs to sequence t
+  const int32_t* pos;
+  int64_t ldk, ldv, n, n_seqs, n_pages, max_pages, total;
+  int32_t Hkv, D, page_shift;
+};
+
+// One thread per 8 features of one token and head.  Bound by latency at one
+// token a sequence; a prompt's tokens write their values 2 bytes at a time
+// into lines that neighbouring positions fill.
+template <typename T>
+__global__ __launch_bounds__(256) void kv_append_kernel(AppendParams p) {
+  const int chunks = p.D / 8;
+  const int64_t stride = int64_t(gridDim.x) * 256;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < p.total; i += stride) {
+    const int c = int(i % chunks);
+    const int64_t th = i / chunks;
+    const int h = int(th % p.Hkv);
+    const int64_t t = th / p.Hkv;
+    const int64_t s = p.seq ? p.seq[t] : t, pos = p.pos[t];
+    if (s < 0 || s >= p.n_seqs || pos < 0 || (pos >> p.page_shift) >= p.max_pages) continue;
+    const int64_t page = p.table[s * p.max_pages + (pos >> p.page_shift)];
+    if (page < 0 || page >= p.n_pages) continue;
+    const int64_t slot = pos & ((int64_t(1) << p.page_shift) - 1);
+    const int64_t head = (page * p.Hkv + h) * (int64_t(p.D) << p.page_shift);
+    const T* k = static_cast<const T*>(p.K) + t * p.ldk + int64_t(h) * p.D + 8 * c;
+    const T* v = static_cast<const T*>(p.V) + t * p.ldv + int64_t(h) * p.D + 8 * c;
+    bf16x8_t kk;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) kk[e] = (__bf16)float(k[e]);
+    *reinterpret_cast<bf16x8_t*>(p.Kp + head + slot * p.D + 8 * c) = kk;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      p.Vp[head + (int64_t(8 * c + e) << p.page_shift) + slot] = (__bf16)float(v[e]);
+  }
+}
+
+int page_shift_of(int page) { return __builtin_ctz(unsigned(page)); }
+int head_tiles_of(int G) { return (G + 15) / 16; }
+
+template <int DC>
+void launch_attn_dc(const AttnParams& p, bool q_f32, uint32_t grid, hipStream_t stream) {
+  const dim3 g(grid), blk(kAttnWaves * 64);
+  if (q_f32) {
+    if (p.o_f32) launch((attn_decode_kernel<DC, float, 3>), g, blk, 0u, stream, p);
+    else launch((attn_decode_kernel<DC, float, 2>), g, blk, 0u, stream, p);
+  } else {
+    if (p.o_f32) launch((attn_decode_kernel<DC, __bf16, 3>), g, blk, 0u, stream, p);
+    else launch((attn_decode_kernel<DC, __bf16, 2>), g, blk, 0u, stream, p);
+  }
+}
+
+}  // namespace
+
+// Workgroups of one (sequence, kv head, head tile): enough that a batch of
+// any size puts about four on every compute unit, as long as each keeps
+// kMinTiles steps when every page of the table is in use.  A sequence shorter
+// than that is cut into as many equal parts (split_tiles).
+int attn_nsplit(int64_t n_seqs, int H, int Hkv, int64_t max_pages, int page) {
+  const int64_t rows = std::max<int64_t>(n_seqs * Hkv * head_tiles_of(H / Hkv), 1);
+  const int64_t tiles = (max_pages * page + kKeys - 1) / kKeys;
+  const int64_t want = (4 * int64_t(device_cu_count()) + rows - 1) / rows;
+  return int(std::max<int64_t>(1, std::min<int64_t>({want, tiles / kMinTiles, kMaxSplit})));
+}
+
+size_t attn_workspace_bytes(int64_t n_seqs, int H, int Hkv, int D, int page, int64_t max_pages) {
+  const int ns = attn_nsplit(n_seqs, H, Hkv, max_pages, page);
+  return ns == 1 ? 0 : size_t(n_seqs) * size_t(H) * size_t(ns) * size_t(D + 2) * 4;
+}
+
+int64_t attn_workgroups(int64_t n_seqs, int H, int Hkv, int page, int64_t max_pages) {
+  return n_seqs * Hkv * head_tiles_of(H / Hkv) * attn_nsplit(n_seqs, H, Hkv, max_pages, page);
+}
+
+aa_status_t launch_attn_decode(const AttnCall& c, hipStream_t stream) {
+  AttnParams p{};
+  p.Q = c.Q;
+  p.K = static_cast<const __bf16*>(c.k_pages);
+  p.V = static_cast<const __bf16*>(c.v_pages);
+  p.table = c.page_table;
+  p.lens = c.lengths;
+  p.O = c.O;
+  p.ldq = c.ldq;
+  p.n_pages = c.n_pages;
+  p.max_pages = c.max_pages;
+  p.B = int(c.n_seqs);
+  p.H = c.n_heads;
+  p.Hkv = c.n_kv_heads;
+  p.G = c.n_heads / c.n_kv_heads;
+  p.D = c.head_dim;
+  p.head_tiles = head_tiles_of(p.G);
+  p.page_shift = page_shift_of(c.page_size);
+  p.nsplit = attn_nsplit(c.n_seqs, c.n_heads, c.n_kv_heads, c.max_pages, c.page_size);
+  p.o_f32 = c.o_dtype == AA_F32;
+  p.scale = c.scale;
+  p.part = static_cast<float*>(c.workspace);
+  p.ml = p.part ? p.part + int64_t(p.B) * p.H * p.nsplit * p.D : nullptr;
+  const uint32_t grid = uint32_t(attn_workgroups(c.n_seqs, c.n_heads, c.n_kv_heads, c.page_size, c.max_pages));
+  const bool q_f32 = c.q_dtype == AA_F32;
+  switch ((p.D + 31) / 32) {
+    case 1: launch_attn_dc<1>(p, q_f32, grid, stream); break;
+    case 2: launch_attn_dc<2>(p, q_f32, grid, stream); break;
+    case 3: launch_attn_dc<3>(p, q_f32, grid, stream); break;
+    case 4: launch_attn_dc<4>(p, q_f32, grid, stream); break;
+    case 5: launch_attn_dc<5>(p, q_f32, grid, stream); break;
+    case 6: launch_attn_dc<6>(p, q_f32, grid, stream); break;
+    case 7: launch_attn_dc<7>(p, q_f32, grid, stream); break;
+    default: launch_attn_dc<8>(p, q_f32, grid, stream); break;
+  }
+  aa_status_t st = after_launch(stream, "attn_decode_kernel");
+  if (st != AA_OK || p.nsplit == 1) return st;
+  launch(attn_join_kernel, dim3(uint32_t(int64_t(p.B) * p.H)), dim3(64), 0u, stream, p);
+  return after_launch(stream, "attn_join_kernel");
+}
+
+aa_status_t launch_kv_append(const AppendCall& c, hipStream_t stream) {
+  AppendParams p{c.K,     c.V,        static_cast<__bf16*>(c.k_pages), static_cast<__bf16*>(c.v_pages),
+                 c.page_table, c.seq, c.pos, c.ldk, c.ldv, c.n, c.n_seqs, c.n_pages, c.max_pages,
+                 c.n * c.n_kv_heads * (c.head_dim / 8), c.n_kv_heads, c.head_dim, page_shift_of(c.page_size)};
+  const int64_t wgs = std::min<int64_t>((p.total + 255) / 256, int64_t(device_cu_count()) * 32);
+  if (c.in_dtype == AA_F32) launch((kv_append_kernel<float>), dim3(uint32_t(wgs)), dim3(256), 0u, stream, p);
+  else launch((kv_append_kernel<__bf16>), dim3(uint32_t(wgs)), dim3(256), 0u, stream, p);
+  return after_launch(stream, "kv_append_kernel");
+}
+
+}  // namespace aa

@@ -92,6 +92,76 @@ aa_status_t launch_bwd_data(const aa_plan_s& plan, const void* dY, const void* W
 aa_status_t launch_bwd_weight(const aa_plan_s& plan, const void* X, const void* dY, void* dW, int64_t M,
                               int64_t pos_offset, void* ws, hipStream_t stream);
 
+// LayerNorm (aa_norm.hip); the members are the arguments of the entry points.
+struct NormFwdCall {
+  const void* X;
+  const void* delta;
+  const float* gamma;
+  const float* beta;
+  void* S;
+  void* Y;
+  float* mean;
+  float* rstd;
+  int64_t M, d;
+  float eps;
+  aa_dtype_t x_dtype, delta_dtype, y_dtype;
+};
+struct NormBwdCall {
+  const void* X;
+  const void* dY;
+  const float* gamma;
+  const float* mean;
+  const float* rstd;
+  const void* dS;
+  void* dX;
+  float* dgamma;
+  float* dbeta;
+  int64_t M, d;
+  aa_dtype_t x_dtype, dy_dtype;
+  float* workspace;
+};
+constexpr int64_t kNormMaxWidth = 32768;
+aa_status_t launch_norm_fwd(const NormFwdCall& call, hipStream_t stream);
+size_t norm_bwd_workspace_bytes(int64_t M, int64_t d);
+aa_status_t launch_norm_bwd(const NormBwdCall& call, hipStream_t stream);
+
+// Paged decode attention and its cache (aa_attn.hip).
+struct AttnCall {
+  const void* Q;
+  int64_t ldq;
+  aa_dtype_t q_dtype;
+  const void* k_pages;
+  const void* v_pages;
+  int64_t n_pages;
+  int32_t page_size, n_heads, n_kv_heads, head_dim;
+  const int32_t* page_table;
+  int64_t n_seqs, max_pages;
+  const int32_t* lengths;
+  float scale;
+  void* O;
+  aa_dtype_t o_dtype;
+  void* workspace;
+};
+struct AppendCall {
+  const void* K;
+  const void* V;
+  int64_t ldk, ldv;
+  aa_dtype_t in_dtype;
+  void* k_pages;
+  void* v_pages;
+  int64_t n_pages;
+  int32_t page_size, n_kv_heads, head_dim;
+  const int32_t* page_table;
+  int64_t n_seqs, max_pages;
+  const int32_t* seq;
+  const int32_t* pos;
+  int64_t n;
+};
+size_t attn_workspace_bytes(int64_t n_seqs, int n_heads, int n_kv_heads, int head_dim, int page_size,
+                            int64_t max_pages);
+aa_status_t launch_attn_decode(const AttnCall& call, hipStream_t stream);
+aa_status_t launch_kv_append(const AppendCall& call, hipStream_t stream);
+
 // Allocation-free SwiGLU: the hidden activation goes to a static device
 // array of this many bytes (one per GPU); noalloc_scratch returns its address
 // on the current device.

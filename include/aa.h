@@ -245,6 +245,89 @@ aa_status_t aa_project_bwd_weight(aa_plan_t plan, const void* X, const void* dY,
                                   int64_t pos_offset, const int32_t* row_types, void* workspace,
                                   size_t workspace_bytes, hipStream_t stream);
 
+/* LayerNorm with the residual add of the sub-layer before it (the norms of the
+ * pilot decoder that hold the FFN; agihunt.info review, model paragraph).  Per
+ * row of d features:
+ *   s = x + delta, rounded to x_dtype and stored in S   (with delta; else s = x)
+ *   mu = mean(s),  r = 1 / sqrt(mean((s - mu)^2) + eps)
+ *   y = (s - mu) r gamma + beta                         (y_dtype)
+ * X is M x d (x_dtype), delta M x d (delta_dtype) or NULL, S M x d (x_dtype),
+ * given exactly when delta is and equal to X to add in place; gamma and beta
+ * are d float32 values or NULL (ones, zeros); mean and rstd receive mu and r
+ * (M float32 each) for the backward pass, or are both NULL.  Y must not
+ * overlap another operand.  1 <= d <= 32768, any width and row count; sums and
+ * statistics are float32, the variance that of the deviations from the mean.
+ * M == 0 is a no-op. */
+aa_status_t aa_layernorm_fwd(const void* X, const void* delta, const float* gamma, const float* beta, void* S,
+                             void* Y, float* mean, float* rstd, int64_t M, int64_t d, float eps,
+                             aa_dtype_t x_dtype, aa_dtype_t delta_dtype, aa_dtype_t y_dtype, hipStream_t stream);
+
+/* The gradients of aa_layernorm_fwd.  X is the normalised input (S where the
+ * forward call had delta), mean and rstd what the forward call stored, dY the
+ * gradient of y (M x d, dy_dtype) and dS the gradient that reaches s on the
+ * residual path (M x d, x_dtype) or NULL.  With xh = (x - mu) r and
+ * g = dy gamma:
+ *   dX = dS + r (g - mean(g) - xh mean(g xh))           (x_dtype; also delta's gradient)
+ *   dgamma = sum over rows of dy xh,  dbeta = sum over rows of dy   (float32)
+ * dX may be dS (in place) and must not overlap another operand otherwise.
+ * dgamma and dbeta may each be NULL; they are overwritten, not accumulated
+ * (zeros for M == 0), and do not depend on the order of execution.
+ * Workspace: at least what aa_layernorm_bwd_workspace reports for M and d (none
+ * without dgamma and dbeta); its contents are overwritten, and calls that share
+ * one must not overlap in time. */
+aa_status_t aa_layernorm_bwd_workspace(int64_t M, int64_t d, size_t* bytes);
+aa_status_t aa_layernorm_bwd(const void* X, const void* dY, const float* gamma, const float* mean, const float* rstd,
+                             const void* dS, void* dX, float* dgamma, float* dbeta, int64_t M, int64_t d,
+                             aa_dtype_t x_dtype, aa_dtype_t dy_dtype, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream);
+
+/* A paged key-value cache: how the pilot decoder's new tokens meet the old
+ * ones (agihunt.info review, row-typing paragraph: at decode the KV cache is
+ * kept and only the new position is computed).  Pages hold page_size positions
+ * (a power of two from 16 to 4096) of every kv head, in bf16:
+ *   k_pages [n_pages][n_kv_heads][page_size][head_dim]
+ *   v_pages [n_pages][n_kv_heads][head_dim][page_size]   (values transposed)
+ * Position j of sequence s is slot j mod page_size of page
+ * page_table[s * max_pages + j / page_size]; entries behind a sequence's last
+ * page are never read.  head_dim is a multiple of 8 up to 256.  Rows of K, V
+ * and Q lie ldk, ldv and ldq elements apart (so they may be parts of one QKV
+ * row) and are aligned to their elements only; the other pointers of type
+ * int32_t are 4-byte aligned.
+ *
+ * aa_kv_append writes n tokens' keys and values (n rows of n_kv_heads x
+ * head_dim, in_dtype, rounded to bf16): token t goes to position pos[t] of
+ * sequence seq[t] (seq NULL: of sequence t, n <= n_seqs).  Tokens whose
+ * sequence, position or page lies outside the cache are not written (pos < 0
+ * marks padding).  No two tokens of a call may share a slot: which of their
+ * values stays would be undefined.  n == 0 is a no-op. */
+aa_status_t aa_kv_append(const void* K, const void* V, int64_t ldk, int64_t ldv, aa_dtype_t in_dtype, void* k_pages,
+                         void* v_pages, int64_t n_pages, int32_t page_size, int32_t n_kv_heads, int32_t head_dim,
+                         const int32_t* page_table, int64_t n_seqs, int64_t max_pages, const int32_t* seq,
+                         const int32_t* pos, int64_t n, hipStream_t stream);
+
+/* Attention of one new token per sequence over that cache.  Query head h of
+ * n_heads shares kv head h / (n_heads / n_kv_heads).  Per sequence s and head:
+ *   s_j = scale q . k_j  for 0 <= j < lengths[s],  p = softmax(s),
+ *   o = sum over j of p_j v_j
+ * Q is n_seqs rows of n_heads x head_dim (q_dtype), O n_seqs x n_heads x
+ * head_dim (o_dtype, dense).  lengths counts the positions to attend to (the
+ * new token's own included, where it has been appended).  A sequence of length
+ * 0 gets zeros; one whose length is negative or beyond its table, or that
+ * needs a page outside [0, n_pages), gets NaN, and nothing outside the cache
+ * is read.  Slots behind a sequence's end may hold anything; an infinite value
+ * before it makes its feature's output infinite or NaN.  Scores, softmax
+ * statistics and sums are float32; neither queries nor probabilities are
+ * rounded to bf16.  Workspace: at least what aa_attn_decode_workspace reports;
+ * its contents are overwritten, and calls that share one must not overlap in
+ * time.  n_seqs == 0 is a no-op. */
+aa_status_t aa_attn_decode_workspace(int64_t n_seqs, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                                     int32_t page_size, int64_t max_pages, size_t* bytes);
+aa_status_t aa_attn_decode(const void* Q, int64_t ldq, aa_dtype_t q_dtype, const void* k_pages, const void* v_pages,
+                           int64_t n_pages, int32_t page_size, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                           const int32_t* page_table, int64_t n_seqs, int64_t max_pages, const int32_t* lengths,
+                           float scale, void* O, aa_dtype_t o_dtype, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream);
+
 /* Kernel timing, for measurement only (no part of the method).  After
  * aa_set_kernel_events(start, stop) the next kernel that a call of this
  * library launches from the calling thread records `start` at the beginning
