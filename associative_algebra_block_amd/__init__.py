@@ -24,7 +24,8 @@ __all__ = [
     "aa_project_fwd", "aa_swiglu_ffn_fwd", "aa_swiglu_ffn_fwd_noalloc", "aa_decode_gemv", "aa_project_bwd_workspace",
     "aa_project_bwd_data", "aa_project_bwd_weight",
     "aa_layernorm_fwd", "aa_layernorm_bwd", "aa_layernorm_bwd_workspace",
-    "aa_kv_append", "aa_attn_decode", "aa_attn_decode_workspace", "aa_set_kernel_events", "aa_status_string", "aa_last_error",
+    "aa_kv_append", "aa_attn_decode", "aa_attn_decode_workspace",
+    "aa_moe_ffn_fwd", "aa_moe_ffn_workspace", "aa_set_kernel_events", "aa_status_string", "aa_last_error",
 ]
 
 AA_LAW_QQ, AA_LAW_Q2XQ2, AA_LAW_DIGRAPH = 0, 1, 2
@@ -78,6 +79,9 @@ _SIGNATURES = {
     "aa_attn_decode": (ctypes.c_int, [_c_p, _c_i64, ctypes.c_int, _c_p, _c_p, _c_i64, _c_i32, _c_i32, _c_i32, _c_i32,
                                       _c_p, _c_i64, _c_i64, _c_p, ctypes.c_float, _c_p, ctypes.c_int, _c_p,
                                       ctypes.c_size_t, _c_p]),
+    "aa_moe_ffn_workspace": (ctypes.c_int, [_c_p, _c_p, _c_i32, _c_i32, _c_i64, ctypes.POINTER(ctypes.c_size_t)]),
+    "aa_moe_ffn_fwd": (ctypes.c_int, [_c_p, _c_p, _c_p, _c_p, _c_i32, _c_i32, _c_i32, _c_p, _c_p, _c_p, _c_p, _c_p,
+                                      _c_p, _c_i64, _c_i64, _c_p, _c_p, ctypes.c_size_t, _c_p]),
     "aa_set_kernel_events": (ctypes.c_int, [_c_p, _c_p]),
     "aa_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "aa_last_error": (ctypes.c_char_p, []),
@@ -499,6 +503,34 @@ def aa_attn_decode(Q, k_pages, v_pages, page_table, lengths, O, scale, workspace
         _tensor(lengths, "lengths", (n_seqs,), _I32, dev), scale,
         _tensor(O, "O", (n_seqs, heads, dim), _FLOATS, dev), _DTYPES[O.dtype], ws, nbytes, _stream(stream)),
         "aa_attn_decode")
+
+
+def aa_moe_ffn_workspace(up: Plan, down: Plan, n_experts: int, top_k: int, M: int) -> int:
+    """Bytes of workspace that aa_moe_ffn_fwd needs."""
+    n = ctypes.c_size_t(0)
+    _check(load().aa_moe_ffn_workspace(up.handle, down.handle, int(n_experts), int(top_k), int(M), ctypes.byref(n)),
+           "aa_moe_ffn_workspace")
+    return int(n.value)
+
+
+def aa_moe_ffn_fwd(up: Plan, down: Plan, X, Wr, Wg_packed, Wu_packed, Wd_packed, Y, top_k, normalize=True,
+                   experts=None, weights=None, workspace=None, pos_offset=0, row_types=None, stream=None):
+    """Y = the mixture-of-experts layer of X [M, D] with the router weight Wr
+    [experts, D] and the experts' packed weights [experts, D * F]; experts and
+    weights ([M, top_k]) receive the choice."""
+    dev = _call_device(X, "X")
+    if X.dim() != 2 or not isinstance(Wr, torch.Tensor) or Wr.dim() != 2:
+        raise ValueError("X and Wr: expected two dimensions")
+    M, E, D, nw = X.shape[0], Wr.shape[0], up.d_in, up.d_in * up.d_out
+    top_k = int(top_k)
+    ws, nbytes = _workspace(workspace, dev)
+    _check(load().aa_moe_ffn_fwd(
+        up.handle, down.handle, _tensor(X, "X", (M, D), _BF16, dev), _tensor(Wr, "Wr", (E, D), _BF16, dev), E, top_k,
+        1 if normalize else 0, _tensor(Wg_packed, "Wg_packed", (E, nw), _BF16, dev),
+        _tensor(Wu_packed, "Wu_packed", (E, nw), _BF16, dev), _tensor(Wd_packed, "Wd_packed", (E, nw), _BF16, dev),
+        _tensor(Y, "Y", (M, D), (down.out_torch_dtype,), dev), _tensor(experts, "experts", (M, top_k), _I32, dev),
+        _tensor(weights, "weights", (M, top_k), _F32, dev), M, int(pos_offset),
+        _tensor(row_types, "row_types", (M,), _I32, dev), ws, nbytes, _stream(stream)), "aa_moe_ffn_fwd")
 
 
 def _event(ev):

@@ -22,7 +22,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libaa.so")
 
 SOURCES = ["aa_plan.cpp", "aa_api.cpp", "aa_kernels.hip", "aa_backward.hip", "aa_small.hip", "aa_tile32.hip",
-           "aa_api_ops.cpp", "aa_norm.hip", "aa_attn.hip"]
+           "aa_api_ops.cpp", "aa_norm.hip", "aa_attn.hip", "aa_moe.hip"]
 ARCH = "gfx950"
 
 # Device-code flags.  Packed fp32 arithmetic is switched off for every HIP

@@ -269,4 +269,89 @@ aa_status_t aa_attn_decode(const void* Q, int64_t ldq, aa_dtype_t q_dtype, const
                                 stream);
 }
 
+// Plans and sizes of the mixture-of-experts calls.
+static aa_status_t check_moe(aa_plan_t up, aa_plan_t down, int32_t n_experts, int32_t top_k, int64_t M,
+                             const char* fn) {
+  if (!up || !down) return fail(AA_ERR_INVALID_ARG, std::string(fn) + ": plan is NULL");
+  if (up->law != down->law || up->q != down->q)
+    return fail(AA_ERR_SHAPE, std::string(fn) + ": up and down plans use different laws or q");
+  if (up->type_kind != down->type_kind || up->period != down->period)
+    return fail(AA_ERR_SHAPE, std::string(fn) + ": up and down plans use different type maps");
+  if (up->d_out != down->d_in || up->d_in != down->d_out)
+    return fail(AA_ERR_SHAPE, std::string(fn) + ": up must map D -> F and down F -> D");
+  if (up->in_dtype != AA_BF16 || down->in_dtype != AA_BF16)
+    return fail(AA_ERR_UNSUPPORTED, std::string(fn) + ": experts need bf16 operands");
+  if (up->law == AA_LAW_DIGRAPH)
+    return fail(AA_ERR_UNSUPPORTED, std::string(fn) + ": digraph plans have no expert kernels");
+  if (up->layout_version != 1 || down->layout_version != 1)
+    return fail(AA_ERR_UNSUPPORTED, std::string(fn) + ": blocks that are not multiples of 16 have no expert kernels");
+  if (up->type_kind == AA_TYPES_BLOCK_ROWS)
+    return fail(AA_ERR_UNSUPPORTED, std::string(fn) + ": block-row typing has no expert kernels");
+  if (n_experts < 1 || top_k < 1)
+    return fail(AA_ERR_INVALID_ARG, std::string(fn) + ": n_experts or top_k is less than 1");
+  if (top_k > n_experts) return fail(AA_ERR_SHAPE, std::string(fn) + ": top_k exceeds n_experts");
+  if (n_experts > aa::kMoeMaxExperts || top_k > aa::kMoeMaxTopK)
+    return fail(AA_ERR_UNSUPPORTED, std::string(fn) + ": more than 512 experts, or more than 64 chosen");
+  if (M < 0) return fail(AA_ERR_INVALID_ARG, std::string(fn) + ": M is negative");
+  if (M > aa::kMoeMaxPairs / top_k)
+    return fail(AA_ERR_UNSUPPORTED, std::string(fn) + ": more than 65535 (token, expert) pairs");
+  return AA_OK;
+}
+
+aa_status_t aa_moe_ffn_workspace(aa_plan_t up, aa_plan_t down, int32_t n_experts, int32_t top_k, int64_t M,
+                                 size_t* bytes) {
+  aa::clear_error();
+  aa_status_t st;
+  if ((st = check_moe(up, down, n_experts, top_k, M, "aa_moe_ffn_workspace")) != AA_OK) return st;
+  if (bytes) *bytes = aa::moe_workspace_bytes(*up, n_experts, top_k, M);
+  return AA_OK;
+}
+
+aa_status_t aa_moe_ffn_fwd(aa_plan_t up, aa_plan_t down, const void* X, const void* Wr, int32_t n_experts,
+                           int32_t top_k, int32_t normalize, const void* Wg_packed, const void* Wu_packed,
+                           const void* Wd_packed, void* Y, int32_t* experts, float* weights, int64_t M,
+                           int64_t pos_offset, const int32_t* row_types, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream) {
+  aa::clear_error();
+  static const char* fn = "aa_moe_ffn_fwd";
+  aa_status_t st;
+  if ((st = check_moe(up, down, n_experts, top_k, M, fn)) != AA_OK) return st;
+  if (pos_offset < 0) return fail(AA_ERR_INVALID_ARG, "aa_moe_ffn_fwd: pos_offset is negative");
+  if (up->type_kind == AA_TYPES_EXPLICIT) {
+    if (!row_types && M > 0) return fail(AA_ERR_INVALID_ARG, "aa_moe_ffn_fwd: explicit type map needs row_types");
+  } else if (row_types) {
+    return fail(AA_ERR_INVALID_ARG, "aa_moe_ffn_fwd: row_types given for a plan without an explicit type map");
+  }
+  if (M == 0) return AA_OK;
+  if (row_types && (st = check_elems(row_types, 4, "row_types", fn)) != AA_OK) return st;
+  if ((st = check_ptr(X, "X", fn)) != AA_OK) return st;
+  if ((st = check_ptr(Wr, "Wr", fn)) != AA_OK) return st;
+  if ((st = check_ptr(Wg_packed, "Wg_packed", fn)) != AA_OK) return st;
+  if ((st = check_ptr(Wu_packed, "Wu_packed", fn)) != AA_OK) return st;
+  if ((st = check_ptr(Wd_packed, "Wd_packed", fn)) != AA_OK) return st;
+  if ((st = check_ptr(Y, "Y", fn)) != AA_OK) return st;
+  if (experts && (st = check_elems(experts, 4, "experts", fn)) != AA_OK) return st;
+  if (weights && (st = check_elems(weights, 4, "weights", fn)) != AA_OK) return st;
+  const size_t need = aa::moe_workspace_bytes(*up, n_experts, top_k, M);
+  if (workspace_bytes < need)
+    return fail(AA_ERR_INVALID_ARG, "aa_moe_ffn_fwd: workspace smaller than aa_moe_ffn_workspace reports");
+  if ((st = check_ptr(workspace, "workspace", fn)) != AA_OK) return st;
+  const size_t E = size_t(n_experts), wb = E * size_t(up->d_in) * size_t(up->d_out) * 2, pairs = size_t(M) * top_k * 4;
+  const Range in[] = {{X, size_t(M) * size_t(up->d_in) * 2, "X"},
+                      {Wr, E * size_t(up->d_in) * 2, "Wr"},
+                      {Wg_packed, wb, "Wg_packed"},
+                      {Wu_packed, wb, "Wu_packed"},
+                      {Wd_packed, wb, "Wd_packed"},
+                      {row_types, size_t(M) * 4, "row_types"},
+                      {Y, size_t(M) * size_t(up->d_in) * elem_size(down->out_dtype), "Y"},
+                      {experts, pairs, "experts"},
+                      {weights, pairs, "weights"},
+                      {workspace, need, "workspace"}};
+  if ((st = check_disjoint(in + 6, 4, in, 10, fn)) != AA_OK) return st;
+  return aa::launch_moe(*up, *down,
+                        {X, Wr, n_experts, top_k, normalize, Wg_packed, Wu_packed, Wd_packed, Y, experts, weights, M,
+                         pos_offset, row_types, workspace},
+                        stream);
+}
+
 }  // extern "C"

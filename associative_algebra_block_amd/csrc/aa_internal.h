@@ -162,6 +162,26 @@ size_t attn_workspace_bytes(int64_t n_seqs, int n_heads, int n_kv_heads, int hea
 aa_status_t launch_attn_decode(const AttnCall& call, hipStream_t stream);
 aa_status_t launch_kv_append(const AppendCall& call, hipStream_t stream);
 
+// Mixture-of-experts layer for a few tokens (aa_moe.hip).
+struct MoeCall {
+  const void* X;
+  const void* Wr;
+  int32_t n_experts, top_k, normalize;
+  const void* Wg;
+  const void* Wu;
+  const void* Wd;
+  void* Y;
+  int32_t* experts;
+  float* weights;
+  int64_t M, pos_offset;
+  const int32_t* row_types;
+  void* workspace;
+};
+constexpr int kMoeMaxExperts = 512, kMoeMaxTopK = 64;
+constexpr int64_t kMoeMaxPairs = 65535;
+size_t moe_workspace_bytes(const aa_plan_s& up, int n_experts, int top_k, int64_t M);
+aa_status_t launch_moe(const aa_plan_s& up, const aa_plan_s& down, const MoeCall& call, hipStream_t stream);
+
 // Allocation-free SwiGLU: the hidden activation goes to a static device
 // array of this many bytes (one per GPU); noalloc_scratch returns its address
 // on the current device.

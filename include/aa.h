@@ -328,6 +328,38 @@ aa_status_t aa_attn_decode(const void* Q, int64_t ldq, aa_dtype_t q_dtype, const
                            float scale, void* O, aa_dtype_t o_dtype, void* workspace, size_t workspace_bytes,
                            hipStream_t stream);
 
+/* A mixture-of-experts layer for a few tokens (generation), whose experts are
+ * SwiGLU feed-forwards in the algebra (the pages' expert shape; agihunt.info
+ * review, projection table).  Per token x of row type tau:
+ *   r_e = x . Wr[e]  for the n_experts rows of the router weight Wr
+ *         (n_experts x D row-major, bf16)
+ *   the top_k experts of the largest r, equal ones by the lower index
+ *   w_e = exp(r_e - max r) / sum over all experts of the same   (normalize 0)
+ *         or over the chosen ones                               (normalize 1)
+ *   y   = sum over the chosen e of w_e FFN_e(x), FFN_e that of
+ *         aa_swiglu_ffn_fwd with the packed weights of expert e
+ * `up`, `down` and the type map are those of aa_swiglu_ffn_fwd (bf16 operands,
+ * layout 1, Q_q or Q2 x Q2, position or explicit types); Wg_packed, Wu_packed
+ * and Wd_packed hold the experts' packed weights one after the other
+ * (n_experts * D * F elements each).  Y is M x D of down's out_dtype; experts
+ * and weights (M x top_k, in the order of the choice) may be NULL.  The logits
+ * are summed in float64, everything else in float32; the hidden activation is
+ * kept in float32 whatever up's out_dtype.  Rows whose explicit type lies
+ * outside [0, q) are not written in any output.  A NaN logit is chosen first
+ * and makes the token's weights NaN.  Limits: n_experts <= 512, top_k <= 64,
+ * M * top_k <= 65535; every (token, expert) pair reads its weights for itself,
+ * so many tokens are better served expert by expert with aa_swiglu_ffn_fwd.
+ * Workspace: at least what aa_moe_ffn_workspace reports; its contents are
+ * overwritten, and calls that share one must not overlap in time.  M == 0 is
+ * a no-op. */
+aa_status_t aa_moe_ffn_workspace(aa_plan_t up, aa_plan_t down, int32_t n_experts, int32_t top_k, int64_t M,
+                                 size_t* bytes);
+aa_status_t aa_moe_ffn_fwd(aa_plan_t up, aa_plan_t down, const void* X, const void* Wr, int32_t n_experts,
+                           int32_t top_k, int32_t normalize, const void* Wg_packed, const void* Wu_packed,
+                           const void* Wd_packed, void* Y, int32_t* experts, float* weights, int64_t M,
+                           int64_t pos_offset, const int32_t* row_types, void* workspace, size_t workspace_bytes,
+                           hipStream_t stream);
+
 /* Kernel timing, for measurement only (no part of the method).  After
  * aa_set_kernel_events(start, stop) the next kernel that a call of this
  * library launches from the calling thread records `start` at the beginning
