@@ -335,35 +335,51 @@ def aa_project_bwd_weight(plan: Plan, X, dY, dW_packed, M=None, pos_offset=0, ro
         _stream(stream)), "aa_project_bwd_weight")
 
 
+# The operators below take tensors only: their sizes and types come from them.
+# Their checks are most of what a call of a few microseconds costs on the host,
+# so each tensor passes one line of tests and the reason is looked for only
+# where that fails; the stream comes from the function behind
+# torch.cuda.current_stream (2.5 against 0.1 us).
+
 def _tensor(t, name, shape, dtypes, device):
     """Device pointer of a dense tensor of the given shape and one of the
-    given dtypes on the given device (None passed through).  The operators
-    below take tensors only: their sizes and types come from them."""
+    given dtypes on the GPU of index `device` (None passed through)."""
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    if not t.is_contiguous():
+    if isinstance(t, torch.Tensor):
+        if t.shape == shape and t.dtype in dtypes and t.get_device() == device and t.is_contiguous():
+            return t.data_ptr()
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+        if t.shape != shape:
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t.get_device() != device:
+            raise ValueError(f"{name}: on {t.device}, expected cuda:{device}")
         raise ValueError(f"{name}: must be contiguous")
-    return t.data_ptr()
+    raise TypeError(f"{name}: expected a tensor")
 
 
 def _call_device(t, name):
-    """The device of a call's first operand, which must be the current one:
-    the launch goes to a stream of the current device."""
+    """The GPU index of a call's first operand, which must be the current
+    device: the launch goes to a stream of the current device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a tensor")
-    if t.device.type != "cuda":
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"{name}: must be a device tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {t.device}, but the current device is {torch.cuda.current_device()}")
-    return t.device
+    if index != torch._C._cuda_getDevice():
+        raise ValueError(f"{name}: on {t.device}, but the current device is {torch._C._cuda_getDevice()}")
+    return index
+
+
+def _stream_on(stream, device):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device.index != device:
+            raise ValueError(f"stream: on {stream.device}, expected cuda:{device}")
+        return stream.cuda_stream
+    return int(stream)
 
 
 def _workspace(workspace, device):
@@ -372,9 +388,9 @@ def _workspace(workspace, device):
         return None, 0
     if not isinstance(workspace, torch.Tensor):
         raise TypeError("workspace: expected a tensor")
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace: must be contiguous and on {device}")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: must be contiguous and on cuda:{device}")
+    return workspace.data_ptr(), workspace.nbytes
 
 
 _FLOATS = (torch.bfloat16, torch.float32)
@@ -386,16 +402,16 @@ def aa_layernorm_fwd(X, gamma, beta, Y, delta=None, S=None, mean=None, rstd=None
     X; with delta the sum goes to S (which may be X).  gamma and beta may be
     None; mean and rstd (M float32 values each) are for the backward pass."""
     dev = _call_device(X, "X")
-    if X.dim() != 2:
+    shape = X.shape
+    if len(shape) != 2:
         raise ValueError("X: expected two dimensions")
-    shape = tuple(X.shape)
     M, d = shape
     _check(load().aa_layernorm_fwd(
         _tensor(X, "X", shape, _FLOATS, dev), _tensor(delta, "delta", shape, _FLOATS, dev),
         _tensor(gamma, "gamma", (d,), _F32, dev), _tensor(beta, "beta", (d,), _F32, dev),
         _tensor(S, "S", shape, (X.dtype,), dev), _tensor(Y, "Y", shape, _FLOATS, dev),
         _tensor(mean, "mean", (M,), _F32, dev), _tensor(rstd, "rstd", (M,), _F32, dev), M, d, eps,
-        _DTYPES[X.dtype], AA_F32 if delta is None else _DTYPES[delta.dtype], _DTYPES[Y.dtype], _stream(stream)),
+        _DTYPES[X.dtype], AA_F32 if delta is None else _DTYPES[delta.dtype], _DTYPES[Y.dtype], _stream_on(stream, dev)),
         "aa_layernorm_fwd")
 
 
@@ -410,9 +426,9 @@ def aa_layernorm_bwd(X, dY, gamma, mean, rstd, dX, dgamma=None, dbeta=None, dS=N
     """Gradients of aa_layernorm_fwd: X is the normalised tensor (S where the
     forward call had delta), dS the residual path's gradient (may be dX)."""
     dev = _call_device(X, "X")
-    if X.dim() != 2:
+    shape = X.shape
+    if len(shape) != 2:
         raise ValueError("X: expected two dimensions")
-    shape = tuple(X.shape)
     M, d = shape
     xt = (X.dtype,)
     ws, nbytes = _workspace(workspace, dev)
@@ -421,7 +437,7 @@ def aa_layernorm_bwd(X, dY, gamma, mean, rstd, dX, dgamma=None, dbeta=None, dS=N
         _tensor(gamma, "gamma", (d,), _F32, dev), _tensor(mean, "mean", (M,), _F32, dev),
         _tensor(rstd, "rstd", (M,), _F32, dev), _tensor(dS, "dS", shape, xt, dev), _tensor(dX, "dX", shape, xt, dev),
         _tensor(dgamma, "dgamma", (d,), _F32, dev), _tensor(dbeta, "dbeta", (d,), _F32, dev), M, d,
-        _DTYPES[X.dtype], _DTYPES[dY.dtype], ws, nbytes, _stream(stream)), "aa_layernorm_bwd")
+        _DTYPES[X.dtype], _DTYPES[dY.dtype], ws, nbytes, _stream_on(stream, dev)), "aa_layernorm_bwd")
 
 
 _I32 = (torch.int32,)
@@ -435,25 +451,27 @@ def _token_rows(t, name, n, heads, dim, dtypes, device):
         raise TypeError(f"{name}: expected a tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    shape, width = tuple(t.shape), heads * dim
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{device}")
+    shape, width = t.shape, heads * dim
     if shape != (n, width) and shape != (n, heads, dim):
-        raise ValueError(f"{name}: shape {shape}, expected {(n, width)} or {(n, heads, dim)}")
-    if t.numel() and (t.stride(-1) != 1 and shape[-1] > 1 or t.dim() == 3 and heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected {(n, width)} or {(n, heads, dim)}")
+    stride = t.stride()
+    if n and (stride[-1] != 1 and shape[-1] > 1 or len(shape) == 3 and heads > 1 and stride[1] != dim):
         raise ValueError(f"{name}: the values of a token must be contiguous")
-    return t.data_ptr(), t.stride(0) if n > 1 else width
+    return t.data_ptr(), stride[0] if n > 1 else width
 
 
 def _cache_sizes(k_pages, v_pages, page_table):
-    """(n_pages, n_kv_heads, page_size, head_dim, n_seqs, max_pages)."""
-    for t, name, dim in ((k_pages, "k_pages", 4), (v_pages, "v_pages", 4), (page_table, "page_table", 2)):
+    """(n_pages, n_kv_heads, page_size, head_dim, n_seqs, max_pages, shapes of the two)."""
+    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages"), (page_table, "page_table")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name}: expected a tensor")
-        if t.dim() != dim:
-            raise ValueError(f"{name}: {t.dim()} dimensions, expected {dim}")
-    n_pages, hkv, page, dim = k_pages.shape
-    return n_pages, hkv, page, dim, page_table.shape[0], page_table.shape[1]
+    kshape, tshape = k_pages.shape, page_table.shape
+    if len(kshape) != 4 or len(tshape) != 2:
+        raise ValueError("k_pages: expected four dimensions, page_table: two")
+    n_pages, hkv, page, dim = kshape
+    return n_pages, hkv, page, dim, tshape[0], tshape[1], kshape, (n_pages, hkv, dim, page), tshape
 
 
 def aa_kv_append(K, V, k_pages, v_pages, page_table, pos, seq=None, stream=None):
@@ -461,18 +479,18 @@ def aa_kv_append(K, V, k_pages, v_pages, page_table, pos, seq=None, stream=None)
     [n, kv heads, head dim], rows of any stride) to their places in the cache:
     token t to position pos[t] of sequence seq[t] (None: sequence t)."""
     dev = _call_device(k_pages, "k_pages")
-    n_pages, hkv, page, dim, n_seqs, max_pages = _cache_sizes(k_pages, v_pages, page_table)
+    n_pages, hkv, page, dim, n_seqs, max_pages, kshape, vshape, tshape = _cache_sizes(k_pages, v_pages, page_table)
     if not isinstance(pos, torch.Tensor) or pos.dim() != 1:
         raise ValueError("pos: expected a tensor of one dimension")
-    n = pos.shape[0]
+    n = len(pos)
     k, ldk = _token_rows(K, "K", n, hkv, dim, _FLOATS, dev)
     v, ldv = _token_rows(V, "V", n, hkv, dim, (K.dtype,), dev)
     _check(load().aa_kv_append(
         k, v, ldk, ldv, _DTYPES[K.dtype],
-        _tensor(k_pages, "k_pages", (n_pages, hkv, page, dim), _BF16, dev),
-        _tensor(v_pages, "v_pages", (n_pages, hkv, dim, page), _BF16, dev), n_pages, page, hkv, dim,
-        _tensor(page_table, "page_table", (n_seqs, max_pages), _I32, dev), n_seqs, max_pages,
-        _tensor(seq, "seq", (n,), _I32, dev), _tensor(pos, "pos", (n,), _I32, dev), n, _stream(stream)),
+        _tensor(k_pages, "k_pages", kshape, _BF16, dev),
+        _tensor(v_pages, "v_pages", vshape, _BF16, dev), n_pages, page, hkv, dim,
+        _tensor(page_table, "page_table", tshape, _I32, dev), n_seqs, max_pages,
+        _tensor(seq, "seq", (n,), _I32, dev), _tensor(pos, "pos", (n,), _I32, dev), n, _stream_on(stream, dev)),
         "aa_kv_append")
 
 
@@ -489,7 +507,7 @@ def aa_attn_decode(Q, k_pages, v_pages, page_table, lengths, O, scale, workspace
     heads * head dim] or [n_seqs, heads, head dim], rows of any stride) over
     the first lengths[s] positions of each sequence."""
     dev = _call_device(k_pages, "k_pages")
-    n_pages, hkv, page, dim, n_seqs, max_pages = _cache_sizes(k_pages, v_pages, page_table)
+    n_pages, hkv, page, dim, n_seqs, max_pages, kshape, vshape, tshape = _cache_sizes(k_pages, v_pages, page_table)
     if not isinstance(O, torch.Tensor) or O.dim() != 3:
         raise ValueError("O: expected a tensor of three dimensions")
     heads = O.shape[1]
@@ -497,11 +515,11 @@ def aa_attn_decode(Q, k_pages, v_pages, page_table, lengths, O, scale, workspace
     ws, nbytes = _workspace(workspace, dev)
     _check(load().aa_attn_decode(
         q, ldq, _DTYPES[Q.dtype],
-        _tensor(k_pages, "k_pages", (n_pages, hkv, page, dim), _BF16, dev),
-        _tensor(v_pages, "v_pages", (n_pages, hkv, dim, page), _BF16, dev), n_pages, page, heads, hkv, dim,
-        _tensor(page_table, "page_table", (n_seqs, max_pages), _I32, dev), n_seqs, max_pages,
+        _tensor(k_pages, "k_pages", kshape, _BF16, dev),
+        _tensor(v_pages, "v_pages", vshape, _BF16, dev), n_pages, page, heads, hkv, dim,
+        _tensor(page_table, "page_table", tshape, _I32, dev), n_seqs, max_pages,
         _tensor(lengths, "lengths", (n_seqs,), _I32, dev), scale,
-        _tensor(O, "O", (n_seqs, heads, dim), _FLOATS, dev), _DTYPES[O.dtype], ws, nbytes, _stream(stream)),
+        _tensor(O, "O", (n_seqs, heads, dim), _FLOATS, dev), _DTYPES[O.dtype], ws, nbytes, _stream_on(stream, dev)),
         "aa_attn_decode")
 
 
@@ -530,7 +548,7 @@ def aa_moe_ffn_fwd(up: Plan, down: Plan, X, Wr, Wg_packed, Wu_packed, Wd_packed,
         _tensor(Wu_packed, "Wu_packed", (E, nw), _BF16, dev), _tensor(Wd_packed, "Wd_packed", (E, nw), _BF16, dev),
         _tensor(Y, "Y", (M, D), (down.out_torch_dtype,), dev), _tensor(experts, "experts", (M, top_k), _I32, dev),
         _tensor(weights, "weights", (M, top_k), _F32, dev), M, int(pos_offset),
-        _tensor(row_types, "row_types", (M,), _I32, dev), ws, nbytes, _stream(stream)), "aa_moe_ffn_fwd")
+        _tensor(row_types, "row_types", (M,), _I32, dev), ws, nbytes, _stream_on(stream, dev)), "aa_moe_ffn_fwd")
 
 
 def _event(ev):
