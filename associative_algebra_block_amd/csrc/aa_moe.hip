@@ -26,8 +26,6 @@
 namespace aa {
 namespace {
 
-constexpr int kPerThread = kMoeMaxExperts / 256;   // experts that one thread of a workgroup ranks
-
 struct MoeParams {
   const __bf16* X;       // [M][D]
   const __bf16* Wr;      // [E][D]
@@ -42,16 +40,15 @@ struct MoeParams {
   int32_t* chosen;       // [M][top_k]
   float* share;          // [M][top_k]
   const int32_t* types;  // or nullptr: by position
-  int64_t M, D, F, off, period;
+  int64_t D, F;
   int32_t E, top_k, q, law, normalize, y_f32;
+  int32_t off;           // position of token 0, modulo q
 };
 
-// The row type of token t; rows of a type outside [0, q) are left alone.
-__device__ inline int row_type(const MoeParams& p, int64_t t) {
-  if (p.types) return p.types[t];
-  int64_t pos = p.off + t;
-  if (p.period) pos %= p.period;
-  return int(pos % p.q);
+// The row type of token t; rows of a type outside [0, q) are left alone.  A
+// period is a multiple of q, so it does not change the type of a position.
+__device__ inline int row_type(const MoeParams& p, int t) {
+  return p.types ? p.types[t] : int(uint32_t(p.off + t) % uint32_t(p.q));
 }
 
 __device__ inline float lo_f(uint32_t v) { return __uint_as_float(v << 16); }
@@ -81,70 +78,102 @@ __global__ __launch_bounds__(256) void moe_router_kernel(MoeParams p) {
   if (lane == 0) p.logits[t * p.E + e] = acc;
 }
 
-// a comes before b in the choice (NaN first, so that it is not lost).
-__device__ inline bool before(double a, int ia, double b, int ib) {
-  const bool na = a != a, nb = b != b;
-  if (na || nb) return na && (!nb || ia < ib);
-  return a > b || (a == b && ia < ib);
+// The order of the choice as that of unsigned integers: larger logits have
+// larger keys, -0 and 0 the same one, NaN (which must not get lost) the largest.
+__device__ inline uint64_t choice_key(double v) {
+  const uint64_t b = uint64_t(__double_as_longlong(v + 0.0));
+  if (v != v) return ~uint64_t(0);
+  return b >> 63 ? ~b : b | uint64_t(1) << 63;
 }
 
-// acc[m] += this lane's part of x_g . (columns of a strip) over the input
-// groups of one leaf, for NM matrices of one layout.  A lane holds run `lane`
-// of every 32-row slab: 8 rows of one column.  off: element offset of the
-// expert; x: the token's row.
-template <int NM, typename TX>
-__device__ inline void strip_dot(const __bf16* const* W, int64_t off, const TX* x, const int* groups, int n_groups,
-                                 int k, int q, int bi, int64_t block, int strip, int lane, float* acc) {
-  constexpr int U = 8;   // steps whose loads are in flight together
-  const int slabs = (bi + 31) / 32;
-  const int steps = n_groups * slabs;
-  const int64_t in_strip = int64_t(strip) * bi * 16;
-  for (int s0 = 0; s0 < steps; s0 += U) {
-    u32x4_t w[U][NM];
-    float xv[U][8];
+// The input groups of a leaf, two to a register: an array that a loop's counter
+// indexes would be kept in memory.
+struct Groups {
+  uint64_t lo, hi;
+  int n;
+};
+__device__ inline Groups leaf_groups_of(int law, int i, int k) {
+  int g[4] = {0, 0, 0, 0};
+  Groups r;
+  r.n = device_leaf_groups(law, i, k, g);
+  r.lo = uint32_t(g[0]) | uint64_t(uint32_t(g[1])) << 32;
+  r.hi = uint32_t(g[2]) | uint64_t(uint32_t(g[3])) << 32;
+  return r;
+}
+
+// acc[m] += the steps begin .. end - 1 of the sum of one strip of 16 columns of
+// output group k, for NM matrices of one layout.  The steps run over the chosen
+// experts (a: its element offset expert_at(a), its factor share(a), activations
+// at x + a * x_stride), the leaf's input groups and the 32-row slabs of a
+// group's block; a lane holds run `lane` of a slab, 8 rows of one column.
+//
+// Lane i works out where step i lies, once for 64 steps, and the wave reads it
+// back a step at a time: done by the scalar unit the addresses took longer than
+// the loads.  Eight steps' loads go out without a branch or a use between them;
+// a step behind the end loads the last one's data again and is left out of the
+// sum, as are the lanes behind the half slab that ends a block of an odd
+// multiple of 16 rows.
+template <int NM, typename TX, typename FAt, typename FShare>
+__device__ inline void strip_dot(const __bf16* const* W, FAt expert_at, const TX* x, int x_stride, FShare share,
+                                 Groups groups, int k, int q, int bi, int64_t block, int strip, int lane, int begin,
+                                 int end, float* acc) {
+  constexpr int U = 8;
+  constexpr int kXRegs = sizeof(TX) / 2;   // 16-byte pieces of 8 activations
+  const int slabs = (bi + 31) / 32, per_expert = groups.n * slabs;
+  const int row = (lane >> 4) * 8;
+  for (int s0 = begin; s0 < end; s0 += 64) {
+    const int s = min(s0 + lane, end - 1);
+    const int a = s / per_expert, in_expert = s - a * per_expert;
+    const int g = in_expert / slabs, slab = in_expert - g * slabs;
+    const int grp = int((g & 2 ? groups.hi : groups.lo) >> (32 * (g & 1)));
+    const int64_t at = expert_at(a) + (int64_t(grp) * q + k) * block + int64_t(strip) * bi * 16 + slab * 512;
+    const int at_lo = int(at), at_hi = int(at >> 32);
+    const int x_at = a * x_stride + grp * bi + slab * 32;
+    const int full = slab * 32 + 32 <= bi;
+    const int sh = __float_as_int(share(a));
+    const int n = min(end - s0, 64);
+    for (int u0 = 0; u0 < n; u0 += U) {
+      u32x4_t w[U][NM], xv[U][kXRegs];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int s = s0 + u;
+      for (int u = 0; u < U; ++u) {
+        const int64_t w_at = int64_t(uint64_t(uint32_t(__builtin_amdgcn_readlane(at_lo, u0 + u))) |
+                                     uint64_t(uint32_t(__builtin_amdgcn_readlane(at_hi, u0 + u))) << 32);
+        const bool whole = __builtin_amdgcn_readlane(full, u0 + u) != 0;
 #pragma unroll
-      for (int m = 0; m < NM; ++m) w[u][m] = u32x4_t{0u, 0u, 0u, 0u};
+        for (int m = 0; m < NM; ++m)
+          w[u][m] = *reinterpret_cast<const u32x4_t*>(W[m] + w_at + (whole ? lane : lane & 31) * 8);
+        const TX* src = x + __builtin_amdgcn_readlane(x_at, u0 + u) + (whole ? row : row & 15);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) xv[u][e] = 0.0f;
-      if (s < steps) {
-        const int gi = s / slabs, slab = s - gi * slabs;
-        const int grp = groups[gi];
-        // the last slab of an odd multiple of 16 rows has half the runs
-        if (slab * 32 + (lane >> 4) * 8 < bi) {
-          const int64_t at = off + (int64_t(grp) * q + k) * block + in_strip + slab * 512 + lane * 8;
+        for (int i = 0; i < kXRegs; ++i) xv[u][i] = reinterpret_cast<const u32x4_t*>(src)[i];
+      }
 #pragma unroll
-          for (int m = 0; m < NM; ++m) w[u][m] = *reinterpret_cast<const u32x4_t*>(W[m] + at);
-          const TX* src = x + int64_t(grp) * bi + slab * 32 + (lane >> 4) * 8;
-          if constexpr (sizeof(TX) == 2) {
-            const u32x4_t v = *reinterpret_cast<const u32x4_t*>(src);
+      for (int u = 0; u < U; ++u) {
+        if (u0 + u >= n) break;
+        const bool ok = lane < 32 || __builtin_amdgcn_readlane(full, u0 + u) != 0;
+        const float factor = __int_as_float(__builtin_amdgcn_readlane(sh, u0 + u));
+        float xf[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              xv[u][2 * j] = lo_f(v[j]);
-              xv[u][2 * j + 1] = hi_f(v[j]);
-            }
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (kXRegs == 1) {
+            xf[2 * j] = lo_f(xv[u][0][j]);
+            xf[2 * j + 1] = hi_f(xv[u][0][j]);
           } else {
-            const f32x4_t a = reinterpret_cast<const f32x4_t*>(src)[0], b = reinterpret_cast<const f32x4_t*>(src)[1];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              xv[u][j] = a[j];
-              xv[u][4 + j] = b[j];
-            }
+            xf[j] = __uint_as_float(xv[u][0][j]);
+            xf[4 + j] = __uint_as_float(xv[u][1][j]);
           }
+        }
+#pragma unroll
+        for (int m = 0; m < NM; ++m) {
+          float part = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            part = fmaf(lo_f(w[u][m][j]), xf[2 * j], part);
+            part = fmaf(hi_f(w[u][m][j]), xf[2 * j + 1], part);
+          }
+          acc[m] += ok ? part * factor : 0.0f;
         }
       }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int m = 0; m < NM; ++m)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          acc[m] = fmaf(lo_f(w[u][m][j]), xv[u][2 * j], acc[m]);
-          acc[m] = fmaf(hi_f(w[u][m][j]), xv[u][2 * j + 1], acc[m]);
-        }
   }
 }
 
@@ -153,104 +182,163 @@ __device__ inline float quad_sum(float v) {   // over the four lanes of a column
   return v + __shfl_xor(v, 32, 64);
 }
 
-// Gate, up and SiLU: one wave per 16 hidden columns of one (token, rank).
-__global__ __launch_bounds__(256) void moe_up_kernel(MoeParams p) {
-  extern __shared__ double s_logit[];   // [E]
-  __shared__ int s_expert, s_first;
-  __shared__ float s_red[4];
-  const int64_t pair = blockIdx.y;
-  const int64_t t = pair / p.top_k;
-  const int rank = int(pair - t * p.top_k);
-  const int tau = row_type(p, t);
-  if (tau < 0 || tau >= p.q) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int e = threadIdx.x; e < p.E; e += 256) s_logit[e] = p.logits[t * p.E + e];
-  __syncthreads();
-  int place[kPerThread];   // this thread's experts' places in the choice
-#pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int e = threadIdx.x + 256 * i;
-    place[i] = p.E;
-    if (e >= p.E) continue;
-    const double v = s_logit[e];
+// places[e] += how many experts o come before e in the choice, over this
+// thread's share of the o; keys in LDS.  By the keys' upper halves alone
+// (exact == false) experts that agree in them get the same place, which the
+// caller sees: two such logits differ by less than 2^-20 of themselves.
+template <bool exact>
+__device__ inline void rank_experts(const uint64_t* keys, const uint32_t* upper, int E, int* places) {
+  const int per = E <= 64 ? 4 : E <= 128 ? 2 : 1;   // threads that share an expert's comparisons
+  const int width = 256 / per, part = threadIdx.x / width;
+  const int begin = part * E / per, end = (part + 1) * E / per;
+  for (int e = threadIdx.x & (width - 1); e < E; e += width) {
+    const uint64_t mine = keys[e];
+    const uint32_t mine_upper = upper[e];
     int r = 0;
-    for (int o = 0; o < p.E; ++o) r += before(s_logit[o], o, v, e) ? 1 : 0;
-    place[i] = r;
-    if (r == rank) s_expert = e;
-    if (r == 0) s_first = e;
+#pragma unroll 16
+    for (int o = begin; o < end; ++o) {
+      if constexpr (exact) r += keys[o] > mine || (keys[o] == mine && o < e) ? 1 : 0;
+      else r += upper[o] > mine_upper ? 1 : 0;
+    }
+    atomicAdd(&places[e], r);
+  }
+}
+
+// Gate, up and SiLU of one (token, rank): WS waves per 16 hidden columns, which
+// share the sum's parts and join in LDS.
+template <int WS>
+__global__ __launch_bounds__(256) void moe_up_kernel(MoeParams p) {
+  extern __shared__ uint64_t s_key[];   // [E], then [E] upper halves and [E] places
+  uint32_t* s_upper = reinterpret_cast<uint32_t*>(s_key + p.E);
+  int* s_place = reinterpret_cast<int*>(s_upper + p.E);
+  __shared__ int s_expert, s_hits[3];
+  __shared__ uint64_t s_top;
+  __shared__ float s_red[4], s_part[4][2][16];
+  const int64_t pair = blockIdx.y;
+  const int64_t t = blockIdx.y / uint32_t(p.top_k);
+  const int rank = int(pair - t * p.top_k);
+  const int tau = row_type(p, int(t));
+  if (tau < 0 || tau >= p.q) return;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+  // This workgroup ranks all experts for itself.  The comparisons of upper
+  // halves are a fifth of the exact ones' work (which took 7 of 30 us with 16
+  // tokens and 128 experts) and nearly always decide; where the first place,
+  // this workgroup's or the border of the choice is shared, all are compared.
+  for (int e = threadIdx.x; e < p.E; e += 256) {
+    const uint64_t key = choice_key(p.logits[t * p.E + e]);
+    s_key[e] = key;
+    s_upper[e] = uint32_t(key >> 32);
+    s_place[e] = 0;
+  }
+  if (threadIdx.x < 3) s_hits[threadIdx.x] = 0;
+  __syncthreads();
+  rank_experts<false>(s_key, s_upper, p.E, s_place);
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += 256) {
+    const int place = s_place[e];
+    if (place == 0) atomicAdd(&s_hits[0], 1);
+    if (place == rank) atomicAdd(&s_hits[1], 1);
+    if (place < p.top_k) atomicAdd(&s_hits[2], 1);
   }
   __syncthreads();
-  const int expert = s_expert;
+  if (s_hits[0] != 1 || s_hits[1] != 1 || s_hits[2] != p.top_k) {   // the same for all threads
+    for (int e = threadIdx.x; e < p.E; e += 256) s_place[e] = 0;
+    __syncthreads();
+    rank_experts<true>(s_key, s_upper, p.E, s_place);
+    __syncthreads();
+  }
+  for (int e = threadIdx.x; e < p.E; e += 256) {
+    if (s_place[e] == rank) s_expert = e;
+    if (s_place[e] == 0) s_top = s_key[e];
+  }
+  __syncthreads();
+  const int expert = __builtin_amdgcn_readfirstlane(s_expert);
   if (blockIdx.x == 0) {   // this pair's weight, for the next kernel and the caller
-    const double top = s_logit[s_first];
-    float mine[kPerThread], sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-      const int e = threadIdx.x + 256 * i;
-      mine[i] = e < p.E ? expf(float(s_logit[e] - top)) : 0.0f;
-      if (!p.normalize || place[i] < p.top_k) sum += mine[i];
+    const uint64_t top_key = s_top;
+    const double top = top_key == ~uint64_t(0) ? double(NAN)
+                       : __longlong_as_double((long long)(top_key >> 63 ? top_key ^ uint64_t(1) << 63 : ~top_key));
+    float sum = 0.0f, mine = 0.0f;
+    for (int e = threadIdx.x; e < p.E; e += 256) {
+      const float x = expf(float(p.logits[t * p.E + e] - top));
+      if (!p.normalize || s_place[e] < p.top_k) sum += x;
+      if (e == expert) mine = x;
     }
 #pragma unroll
     for (int s = 32; s >= 1; s >>= 1) sum += __shfl_xor(sum, s, 64);
     if (lane == 0) s_red[wave] = sum;
     __syncthreads();
     sum = (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]);
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i)
-      if (place[i] == rank) {
-        const float w = mine[i] / sum;
-        p.chosen[pair] = expert;
-        p.share[pair] = w;
-        if (p.experts) p.experts[pair] = expert;
-        if (p.weights) p.weights[pair] = w;
-      }
+    if (threadIdx.x == (expert & 255)) {
+      const float w = mine / sum;
+      p.chosen[pair] = expert;
+      p.share[pair] = w;
+      if (p.experts) p.experts[pair] = expert;
+      if (p.weights) p.weights[pair] = w;
+    }
   }
-  const int bi = int(p.D / p.q), bo = int(p.F / p.q);
+
+  const int bi = int(uint32_t(p.D) / uint32_t(p.q)), bo = int(uint32_t(p.F) / uint32_t(p.q));
   const int strips = bo / 16;
-  const int s = blockIdx.x * 4 + wave;   // strip of the whole hidden row
-  if (s >= p.q * strips) return;
+  const int s = blockIdx.x * (4 / WS) + wave / WS;   // strip of the whole hidden row
+  const bool live = s < p.q * strips;
   const int k = s / strips, strip = s - k * strips;
-  int groups[4];
-  const int ng = device_leaf_groups(p.law, tau, k, groups);
-  const __bf16* W[2] = {p.Wg, p.Wu};
   float acc[2] = {0.0f, 0.0f};
-  strip_dot<2>(W, int64_t(expert) * p.D * p.F, p.X + t * p.D, groups, ng, k, p.q, bi, int64_t(bi) * bo, strip, lane,
-               acc);
-  const float g = quad_sum(acc[0]), u = quad_sum(acc[1]);
-  if (lane < 16) p.h[pair * p.F + int64_t(k) * bo + strip * 16 + lane] = g / (1.0f + expf(-g)) * u;
+  if (live) {
+    const Groups groups = leaf_groups_of(p.law, tau, k);
+    const __bf16* W[2] = {p.Wg, p.Wu};
+    const int64_t base = int64_t(expert) * p.D * p.F;
+    const int steps = groups.n * ((bi + 31) / 32), w = wave % WS;
+    strip_dot<2>(W, [&](int) { return base; }, p.X + t * p.D, 0, [](int) { return 1.0f; }, groups, k, p.q, bi,
+                 int64_t(bi) * bo, strip, lane, w * steps / WS, (w + 1) * steps / WS, acc);
+  }
+  float g = quad_sum(acc[0]), u = quad_sum(acc[1]);
+  if constexpr (WS > 1) {
+    if (lane < 16) {
+      s_part[wave][0][lane] = g;
+      s_part[wave][1][lane] = u;
+    }
+    __syncthreads();
+    if (wave % WS != 0) return;
+#pragma unroll
+    for (int v = 1; v < WS; ++v) {
+      g += s_part[wave + v][0][lane & 15];
+      u += s_part[wave + v][1][lane & 15];
+    }
+  }
+  if (live && lane < 16) p.h[pair * p.F + int64_t(k) * bo + strip * 16 + lane] = g / (1.0f + expf(-g)) * u;
 }
 
 // Down projection and weighted sum: a workgroup per 16 output columns of a
-// token; its waves take the chosen experts in turn and join in a fixed order.
+// token.  Its four waves share the parts of the sum over the chosen experts
+// and join in a fixed order.
 __global__ __launch_bounds__(256) void moe_down_kernel(MoeParams p) {
   __shared__ float s_part[4][16];
   const int64_t t = blockIdx.y;
-  const int tau = row_type(p, t);
+  const int tau = row_type(p, int(t));
   if (tau < 0 || tau >= p.q) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int bi = int(p.F / p.q), bo = int(p.D / p.q);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int bi = int(uint32_t(p.F) / uint32_t(p.q)), bo = int(uint32_t(p.D) / uint32_t(p.q));
   const int strips = bo / 16;
   const int k = blockIdx.x / strips, strip = blockIdx.x - k * strips;
-  int groups[4];
-  const int ng = device_leaf_groups(p.law, tau, k, groups);
+  const Groups groups = leaf_groups_of(p.law, tau, k);
   const __bf16* W[1] = {p.Wd};
-  float y = 0.0f;
-  for (int a = wave; a < p.top_k; a += 4) {
-    const int64_t pair = t * p.top_k + a;
-    float acc[1] = {0.0f};
-    strip_dot<1>(W, int64_t(p.chosen[pair]) * p.D * p.F, p.h + pair * p.F, groups, ng, k, p.q, bi,
-                 int64_t(bi) * bo, strip, lane, acc);
-    y = fmaf(p.share[pair], acc[0], y);
-  }
-  y = quad_sum(y);
+  const int32_t* chosen = p.chosen + t * p.top_k;
+  const float* weight = p.share + t * p.top_k;
+  const int steps = p.top_k * groups.n * ((bi + 31) / 32);
+  float acc[1] = {0.0f};
+  strip_dot<1>(W, [&](int a) { return int64_t(chosen[a]) * p.D * p.F; }, p.h + t * p.top_k * p.F, int(p.F),
+               [&](int a) { return weight[a]; }, groups, k, p.q, bi, int64_t(bi) * bo, strip, lane, wave * steps / 4,
+               (wave + 1) * steps / 4, acc);
+  const float y = quad_sum(acc[0]);
   if (lane < 16) s_part[wave][lane] = y;
   __syncthreads();
   if (threadIdx.x < 16) {
     const int c = threadIdx.x;
-    y = (s_part[0][c] + s_part[1][c]) + (s_part[2][c] + s_part[3][c]);
+    const float v = (s_part[0][c] + s_part[1][c]) + (s_part[2][c] + s_part[3][c]);
     const int64_t at = t * p.D + int64_t(k) * bo + strip * 16 + c;
-    if (p.y_f32) static_cast<float*>(p.Y)[at] = y;
-    else static_cast<__bf16*>(p.Y)[at] = (__bf16)y;
+    if (p.y_f32) static_cast<float*>(p.Y)[at] = v;
+    else static_cast<__bf16*>(p.Y)[at] = (__bf16)v;
   }
 }
 
@@ -293,11 +381,9 @@ aa_status_t launch_moe(const aa_plan_s& up, const aa_plan_s& down, const MoeCall
   p.chosen = reinterpret_cast<int32_t*>(ws + sp.chosen);
   p.share = reinterpret_cast<float*>(ws + sp.share);
   p.types = c.row_types;
-  p.M = c.M;
   p.D = up.d_in;
   p.F = up.d_out;
-  p.period = up.period;
-  p.off = c.pos_offset % (up.period ? up.period : up.q);
+  p.off = int32_t(c.pos_offset % up.q);
   p.E = c.n_experts;
   p.top_k = c.top_k;
   p.q = up.q;
@@ -308,7 +394,10 @@ aa_status_t launch_moe(const aa_plan_s& up, const aa_plan_s& down, const MoeCall
   launch(moe_router_kernel, dim3((p.E + 3) / 4, M), dim3(256), 0u, stream, p);
   aa_status_t st = after_launch(stream, "moe_router_kernel");
   if (st != AA_OK) return st;
-  launch(moe_up_kernel, dim3(uint32_t((p.F / 16 + 3) / 4), pairs), dim3(256), uint32_t(p.E * 8), stream, p);
+  const uint32_t strips = uint32_t(p.F / 16), lds = uint32_t(p.E * 16);
+  if (pairs * strips <= 1024) launch((moe_up_kernel<4>), dim3(strips, pairs), dim3(256), lds, stream, p);
+  else if (pairs * strips <= 2048) launch((moe_up_kernel<2>), dim3((strips + 1) / 2, pairs), dim3(256), lds, stream, p);
+  else launch((moe_up_kernel<1>), dim3((strips + 3) / 4, pairs), dim3(256), lds, stream, p);
   st = after_launch(stream, "moe_up_kernel");
   if (st != AA_OK) return st;
   launch(moe_down_kernel, dim3(uint32_t(p.D / 16), M), dim3(256), 0u, stream, p);
