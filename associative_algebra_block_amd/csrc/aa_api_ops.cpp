@@ -287,6 +287,8 @@ static aa_status_t check_moe(aa_plan_t up, aa_plan_t down, int32_t n_experts, in
     return fail(AA_ERR_UNSUPPORTED, std::string(fn) + ": blocks that are not multiples of 16 have no expert kernels");
   if (up->type_kind == AA_TYPES_BLOCK_ROWS)
     return fail(AA_ERR_UNSUPPORTED, std::string(fn) + ": block-row typing has no expert kernels");
+  if (up->d_in >= int64_t(1) << 24 || up->d_out >= int64_t(1) << 24)
+    return fail(AA_ERR_UNSUPPORTED, std::string(fn) + ": widths of 2^24 or more");
   if (n_experts < 1 || top_k < 1)
     return fail(AA_ERR_INVALID_ARG, std::string(fn) + ": n_experts or top_k is less than 1");
   if (top_k > n_experts) return fail(AA_ERR_SHAPE, std::string(fn) + ": top_k exceeds n_experts");

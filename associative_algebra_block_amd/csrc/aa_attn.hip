@@ -268,32 +268,59 @@ __global__ __launch_bounds__(kAttnWaves * 64) void attn_decode_kernel(AttnParams
   }
 }
 
-// Joins the splits of one (sequence, head): one workgroup of 64 lanes each.
-__global__ __launch_bounds__(64) void attn_join_kernel(AttnParams p) {
+// Joins the splits of one (sequence, head): a thread per split for the maximum
+// and the sum, then the threads as groups of `lanes` (a power of two that holds
+// a row in pieces of four features) that take the splits in turn and join in
+// LDS, all in a fixed order.  One group per split in turn took 17.7 us for 32
+// heads of 128 splits, whose loads all waited for one another; this takes 4.
+__global__ __launch_bounds__(kMaxSplit) void attn_join_kernel(AttnParams p, int lanes) {
+  __shared__ float s_w[kMaxSplit], s_red[2][kMaxSplit / 64];
+  __shared__ float s_o[kMaxSplit * 4];
   const int64_t out = blockIdx.x;
-  const int b = int(out / p.H);
-  int64_t len = p.lens[b];
+  const int b = int(blockIdx.x / uint32_t(p.H));
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int32_t length = p.lens[b];
+  int64_t len = length;
   if (len < 0 || len > (p.max_pages << p.page_shift)) len = 0;   // split 0 wrote a NaN
   int used;
   split_tiles(len, p.nsplit, 0, &used);
   used = max(used, 1);
   const float* ml = p.ml + 2 * out * p.nsplit;
-  float mm = -INFINITY;
-  for (int s = threadIdx.x; s < used; s += 64) mm = fmaxf(mm, ml[2 * s]);
+  const float m = tid < used ? ml[2 * tid] : -INFINITY;
+  const float l = tid < used ? ml[2 * tid + 1] : 0.0f;
+  float mm = m;
 #pragma unroll
   for (int x = 32; x >= 1; x >>= 1) mm = fmaxf(mm, __shfl_xor(mm, x, 64));
-  const float mu = mm == -INFINITY ? 0.0f : mm;
-  for (int f = threadIdx.x; f < p.D; f += 64) {
-    float ll = 0.0f, o = 0.0f;
+  if (lane == 0) s_red[0][wave] = mm;
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < kMaxSplit / 64; ++v) mm = fmaxf(mm, s_red[0][v]);
+  const float w = __builtin_amdgcn_exp2f(m - (mm == -INFINITY ? 0.0f : mm));
+  s_w[tid] = w;
+  float sum = tid < used ? w * l : 0.0f;
+#pragma unroll
+  for (int x = 32; x >= 1; x >>= 1) sum += __shfl_xor(sum, x, 64);
+  if (lane == 0) s_red[1][wave] = sum;
+  __syncthreads();
+  sum = 0.0f;
+#pragma unroll
+  for (int v = 0; v < kMaxSplit / 64; ++v) sum += s_red[1][v];
+
+  const int groups = kMaxSplit / lanes, group = tid / lanes, f = 4 * (tid & (lanes - 1));
+  f32x4_t o = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (f < p.D) {
+    const float* part = p.part + out * p.nsplit * p.D + f;
 #pragma unroll 8
-    for (int s = 0; s < used; ++s) {
-      const float e = __builtin_amdgcn_exp2f(ml[2 * s] - mu);
-      ll += e * ml[2 * s + 1];
-      o += e * p.part[(out * p.nsplit + s) * p.D + f];
-    }
-    o = p.lens[b] == 0 ? 0.0f : o / ll;
-    if (p.o_f32) static_cast<float*>(p.O)[out * p.D + f] = o;
-    else static_cast<__bf16*>(p.O)[out * p.D + f] = (__bf16)o;
+    for (int s = group; s < used; s += groups) o += *reinterpret_cast<const f32x4_t*>(part + int64_t(s) * p.D) * s_w[s];
+  }
+  *reinterpret_cast<f32x4_t*>(&s_o[4 * tid]) = o;   // [group][4 lanes]
+  __syncthreads();
+  if (tid < p.D) {
+    float v = 0.0f;
+    for (int g = 0; g < min(groups, used); ++g) v += s_o[4 * lanes * g + tid];
+    v = length == 0 ? 0.0f : v / sum;
+    if (p.o_f32) static_cast<float*>(p.O)[out * p.D + tid] = v;
+    else static_cast<__bf16*>(p.O)[out * p.D + tid] = (__bf16)v;
   }
 }
 
@@ -413,7 +440,9 @@ aa_status_t launch_attn_decode(const AttnCall& c, hipStream_t stream) {
   }
   aa_status_t st = after_launch(stream, "attn_decode_kernel");
   if (st != AA_OK || p.nsplit == 1) return st;
-  launch(attn_join_kernel, dim3(uint32_t(int64_t(p.B) * p.H)), dim3(64), 0u, stream, p);
+  int lanes = 2;
+  while (4 * lanes < p.D) lanes *= 2;
+  launch(attn_join_kernel, dim3(uint32_t(int64_t(p.B) * p.H)), dim3(kMaxSplit), 0u, stream, p, lanes);
   return after_launch(stream, "attn_join_kernel");
 }
 

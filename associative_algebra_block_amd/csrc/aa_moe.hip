@@ -109,15 +109,16 @@ __device__ inline Groups leaf_groups_of(int law, int i, int k) {
 //
 // Lane i works out where step i lies, once for 64 steps, and the wave reads it
 // back a step at a time: done by the scalar unit the addresses took longer than
-// the loads.  Eight steps' loads go out without a branch or a use between them;
-// a step behind the end loads the last one's data again and is left out of the
-// sum, as are the lanes behind the half slab that ends a block of an odd
-// multiple of 16 rows.
+// the loads.  U steps' loads go out without a branch or a use between them (8,
+// or 4 with two matrices: at 8 those take 115 registers and fewer waves fit,
+// 22.7 against 19.3 us for 16 tokens); a step behind the end loads the last
+// one's data again and is left out of the sum, as are the lanes behind the half
+// slab that ends a block of an odd multiple of 16 rows.
 template <int NM, typename TX, typename FAt, typename FShare>
 __device__ inline void strip_dot(const __bf16* const* W, FAt expert_at, const TX* x, int x_stride, FShare share,
                                  Groups groups, int k, int q, int bi, int64_t block, int strip, int lane, int begin,
                                  int end, float* acc) {
-  constexpr int U = 8;
+  constexpr int U = NM == 2 ? 4 : 8;
   constexpr int kXRegs = sizeof(TX) / 2;   // 16-byte pieces of 8 activations
   const int slabs = (bi + 31) / 32, per_expert = groups.n * slabs;
   const int row = (lane >> 4) * 8;
@@ -186,10 +187,11 @@ __device__ inline float quad_sum(float v) {   // over the four lanes of a column
 // thread's share of the o; keys in LDS.  By the keys' upper halves alone
 // (exact == false) experts that agree in them get the same place, which the
 // caller sees: two such logits differ by less than 2^-20 of themselves.
+constexpr int kUpWaves = 8, kUpThreads = 64 * kUpWaves;
 template <bool exact>
 __device__ inline void rank_experts(const uint64_t* keys, const uint32_t* upper, int E, int* places) {
-  const int per = E <= 64 ? 4 : E <= 128 ? 2 : 1;   // threads that share an expert's comparisons
-  const int width = 256 / per, part = threadIdx.x / width;
+  const int per = E <= 64 ? 8 : E <= 128 ? 4 : E <= 256 ? 2 : 1;   // threads that share an expert's comparisons
+  const int width = kUpThreads / per, part = threadIdx.x / width;
   const int begin = part * E / per, end = (part + 1) * E / per;
   for (int e = threadIdx.x & (width - 1); e < E; e += width) {
     const uint64_t mine = keys[e];
@@ -207,13 +209,13 @@ __device__ inline void rank_experts(const uint64_t* keys, const uint32_t* upper,
 // Gate, up and SiLU of one (token, rank): WS waves per 16 hidden columns, which
 // share the sum's parts and join in LDS.
 template <int WS>
-__global__ __launch_bounds__(256) void moe_up_kernel(MoeParams p) {
+__global__ __launch_bounds__(kUpThreads) void moe_up_kernel(MoeParams p) {
   extern __shared__ uint64_t s_key[];   // [E], then [E] upper halves and [E] places
   uint32_t* s_upper = reinterpret_cast<uint32_t*>(s_key + p.E);
   int* s_place = reinterpret_cast<int*>(s_upper + p.E);
   __shared__ int s_expert, s_hits[3];
   __shared__ uint64_t s_top;
-  __shared__ float s_red[4], s_part[4][2][16];
+  __shared__ float s_red[kUpWaves], s_part[kUpWaves][2][16];
   const int64_t pair = blockIdx.y;
   const int64_t t = blockIdx.y / uint32_t(p.top_k);
   const int rank = int(pair - t * p.top_k);
@@ -225,7 +227,7 @@ __global__ __launch_bounds__(256) void moe_up_kernel(MoeParams p) {
   // halves are a fifth of the exact ones' work (which took 7 of 30 us with 16
   // tokens and 128 experts) and nearly always decide; where the first place,
   // this workgroup's or the border of the choice is shared, all are compared.
-  for (int e = threadIdx.x; e < p.E; e += 256) {
+  for (int e = threadIdx.x; e < p.E; e += kUpThreads) {
     const uint64_t key = choice_key(p.logits[t * p.E + e]);
     s_key[e] = key;
     s_upper[e] = uint32_t(key >> 32);
@@ -235,7 +237,7 @@ __global__ __launch_bounds__(256) void moe_up_kernel(MoeParams p) {
   __syncthreads();
   rank_experts<false>(s_key, s_upper, p.E, s_place);
   __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += 256) {
+  for (int e = threadIdx.x; e < p.E; e += kUpThreads) {
     const int place = s_place[e];
     if (place == 0) atomicAdd(&s_hits[0], 1);
     if (place == rank) atomicAdd(&s_hits[1], 1);
@@ -243,12 +245,12 @@ __global__ __launch_bounds__(256) void moe_up_kernel(MoeParams p) {
   }
   __syncthreads();
   if (s_hits[0] != 1 || s_hits[1] != 1 || s_hits[2] != p.top_k) {   // the same for all threads
-    for (int e = threadIdx.x; e < p.E; e += 256) s_place[e] = 0;
+    for (int e = threadIdx.x; e < p.E; e += kUpThreads) s_place[e] = 0;
     __syncthreads();
     rank_experts<true>(s_key, s_upper, p.E, s_place);
     __syncthreads();
   }
-  for (int e = threadIdx.x; e < p.E; e += 256) {
+  for (int e = threadIdx.x; e < p.E; e += kUpThreads) {
     if (s_place[e] == rank) s_expert = e;
     if (s_place[e] == 0) s_top = s_key[e];
   }
@@ -259,7 +261,7 @@ __global__ __launch_bounds__(256) void moe_up_kernel(MoeParams p) {
     const double top = top_key == ~uint64_t(0) ? double(NAN)
                        : __longlong_as_double((long long)(top_key >> 63 ? top_key ^ uint64_t(1) << 63 : ~top_key));
     float sum = 0.0f, mine = 0.0f;
-    for (int e = threadIdx.x; e < p.E; e += 256) {
+    for (int e = threadIdx.x; e < p.E; e += kUpThreads) {
       const float x = expf(float(p.logits[t * p.E + e] - top));
       if (!p.normalize || s_place[e] < p.top_k) sum += x;
       if (e == expert) mine = x;
@@ -268,8 +270,10 @@ __global__ __launch_bounds__(256) void moe_up_kernel(MoeParams p) {
     for (int s = 32; s >= 1; s >>= 1) sum += __shfl_xor(sum, s, 64);
     if (lane == 0) s_red[wave] = sum;
     __syncthreads();
-    sum = (s_red[0] + s_red[1]) + (s_red[2] + s_red[3]);
-    if (threadIdx.x == (expert & 255)) {
+    sum = s_red[0];
+#pragma unroll
+    for (int v = 1; v < kUpWaves; ++v) sum += s_red[v];
+    if (threadIdx.x == (expert & (kUpThreads - 1))) {
       const float w = mine / sum;
       p.chosen[pair] = expert;
       p.share[pair] = w;
@@ -280,7 +284,7 @@ __global__ __launch_bounds__(256) void moe_up_kernel(MoeParams p) {
 
   const int bi = int(uint32_t(p.D) / uint32_t(p.q)), bo = int(uint32_t(p.F) / uint32_t(p.q));
   const int strips = bo / 16;
-  const int s = blockIdx.x * (4 / WS) + wave / WS;   // strip of the whole hidden row
+  const int s = blockIdx.x * (kUpWaves / WS) + wave / WS;   // strip of the whole hidden row
   const bool live = s < p.q * strips;
   const int k = s / strips, strip = s - k * strips;
   float acc[2] = {0.0f, 0.0f};
@@ -395,9 +399,10 @@ aa_status_t launch_moe(const aa_plan_s& up, const aa_plan_s& down, const MoeCall
   aa_status_t st = after_launch(stream, "moe_router_kernel");
   if (st != AA_OK) return st;
   const uint32_t strips = uint32_t(p.F / 16), lds = uint32_t(p.E * 16);
-  if (pairs * strips <= 1024) launch((moe_up_kernel<4>), dim3(strips, pairs), dim3(256), lds, stream, p);
-  else if (pairs * strips <= 2048) launch((moe_up_kernel<2>), dim3((strips + 1) / 2, pairs), dim3(256), lds, stream, p);
-  else launch((moe_up_kernel<1>), dim3((strips + 3) / 4, pairs), dim3(256), lds, stream, p);
+  const dim3 block(kUpThreads);
+  if (pairs * strips <= 1024) launch((moe_up_kernel<4>), dim3((strips + 1) / 2, pairs), block, lds, stream, p);
+  else if (pairs * strips <= 2048) launch((moe_up_kernel<2>), dim3((strips + 3) / 4, pairs), block, lds, stream, p);
+  else launch((moe_up_kernel<1>), dim3((strips + 7) / 8, pairs), block, lds, stream, p);
   st = after_launch(stream, "moe_up_kernel");
   if (st != AA_OK) return st;
   launch(moe_down_kernel, dim3(uint32_t(p.D / 16), M), dim3(256), 0u, stream, p);
