@@ -33,7 +33,8 @@ namespace {
 
 constexpr int kKeys = 32;        // keys of one step of a wave
 constexpr int kAttnWaves = 4;
-constexpr int kMinTiles = 8;     // steps of a workgroup below which a sequence is not split further
+constexpr int kMinTiles = 8;     // steps of a workgroup below which a sequence is never split further
+constexpr int kFullTiles = 32;   // steps that repay a workgroup's start and join
 constexpr int kMaxSplit = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -50,7 +51,7 @@ struct AttnParams {
   float* part;       // [B H][nsplit][D], unnormalised
   float* ml;         // [B H][nsplit][2]: running maximum (log2 scale) and sum
   int64_t ldq, n_pages, max_pages;
-  int32_t B, H, Hkv, G, D, head_tiles, page_shift, nsplit, o_f32;
+  int32_t B, H, Hkv, G, D, head_tiles, page_shift, nsplit, min_tiles, o_f32;
   float scale;
 };
 
@@ -58,9 +59,9 @@ struct AttnParams {
 struct TileRange {
   int64_t begin, end;
 };
-__device__ inline TileRange split_tiles(int64_t len, int nsplit, int s, int* used) {
+__device__ inline TileRange split_tiles(int64_t len, int nsplit, int min_tiles, int s, int* used) {
   const int64_t tiles = (len + kKeys - 1) / kKeys;
-  const int64_t per = max((tiles + nsplit - 1) / nsplit, int64_t(kMinTiles));
+  const int64_t per = max((tiles + nsplit - 1) / nsplit, int64_t(min_tiles));
   *used = int((tiles + per - 1) / per);
   return {min(s * per, tiles), min((s + 1) * per, tiles)};
 }
@@ -90,13 +91,15 @@ __global__ __launch_bounds__(kAttnWaves * 64) void attn_decode_kernel(AttnParams
 
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n = lane & 15, g = lane >> 4;
-  int64_t w = blockIdx.x;
-  const int split = int(w % p.nsplit);
-  w /= p.nsplit;
-  const int ht = int(w % p.head_tiles);
-  w /= p.head_tiles;
-  const int hkv = int(w % p.Hkv);
-  const int b = int(w / p.Hkv);
+  // parts outermost: consecutive workgroups go to different dies, and the parts
+  // that only long sequences have spread over all of them (with the parts
+  // innermost, eight of them tied each part to one die: 139 against 116 us)
+  uint32_t w = blockIdx.x;
+  const int ht = int(w % uint32_t(p.head_tiles));
+  w /= uint32_t(p.head_tiles);
+  const int hkv = int(w % uint32_t(p.Hkv));
+  w /= uint32_t(p.Hkv);
+  const int b = int(w % uint32_t(p.B)), split = int(w / uint32_t(p.B));
   const int heads = min(16, p.G - 16 * ht);              // query heads of this workgroup
   const int head0 = hkv * p.G + 16 * ht;
 
@@ -104,7 +107,7 @@ __global__ __launch_bounds__(kAttnWaves * 64) void attn_decode_kernel(AttnParams
   bool bad = len < 0 || len > (p.max_pages << p.page_shift);
   if (bad) len = 0;
   int used;
-  const TileRange r = split_tiles(len, p.nsplit, split, &used);
+  const TileRange r = split_tiles(len, p.nsplit, p.min_tiles, split, &used);
   if (split >= max(used, 1)) return;
 
   // queries: lane n holds features 32 c + 8 g .. + 7 of head n
@@ -136,12 +139,20 @@ __global__ __launch_bounds__(kAttnWaves * 64) void attn_decode_kernel(AttnParams
   const int64_t page_mask = (int64_t(1) << p.page_shift) - 1;
   const int32_t* row = p.table + b * p.max_pages;
 
+  // Positions behind the end read the last one's place: their scores are masked
+  // and their values zeroed below.  The page ids of a step are read while the
+  // step before it computes: read on demand they put a second latency in front
+  // of every step's loads.
+  int kid = 0, vid = 0;
+  auto read_ids = [&](int64_t tile) {
+    kid = row[min(tile * kKeys + 8 * (n >> 2), last) >> p.page_shift];
+    vid = row[min(tile * kKeys + 8 * g, last) >> p.page_shift];
+  };
+  if (r.begin + wave < r.end) read_ids(r.begin + wave);
   for (int64_t tile = r.begin + wave; tile < r.end; tile += kAttnWaves) {
-    // positions behind the end read the last one's place: their scores are
-    // masked and their values zeroed below
     const int64_t kkey = tile * kKeys + 8 * (n >> 2);           // the key fragments' group of 8
     const int64_t vkey = min(tile * kKeys + 8 * g, last & ~int64_t(7));
-    int64_t kpage = row[min(kkey, last) >> p.page_shift], vpage = row[vkey >> p.page_shift];
+    int64_t kpage = kid, vpage = vid;
     const bool wrong = kpage < 0 || kpage >= p.n_pages || vpage < 0 || vpage >= p.n_pages;
     if (wrong) kpage = vpage = 0;
     bad |= wrong;
@@ -162,6 +173,7 @@ __global__ __launch_bounds__(kAttnWaves * 64) void attn_decode_kernel(AttnParams
       const int f = min(16 * d + n, p.D - 1);
       vf[d] = *reinterpret_cast<const u32x4_t*>(vbase + (int64_t(f) << p.page_shift));
     }
+    if (tile + kAttnWaves < r.end) read_ids(tile + kAttnWaves);
     // features behind D: zero (a zero query alone would turn an infinite key into a NaN)
 #pragma unroll
     for (int c = DC - 1; c < DC; ++c)
@@ -283,7 +295,7 @@ __global__ __launch_bounds__(kMaxSplit) void attn_join_kernel(AttnParams p, int 
   int64_t len = length;
   if (len < 0 || len > (p.max_pages << p.page_shift)) len = 0;   // split 0 wrote a NaN
   int used;
-  split_tiles(len, p.nsplit, 0, &used);
+  split_tiles(len, p.nsplit, p.min_tiles, 0, &used);
   used = max(used, 1);
   const float* ml = p.ml + 2 * out * p.nsplit;
   const float m = tid < used ? ml[2 * tid] : -INFINITY;
@@ -383,14 +395,17 @@ void launch_attn_dc(const AttnParams& p, bool q_f32, uint32_t grid, hipStream_t 
 
 }  // namespace
 
-// Workgroups of one (sequence, kv head, head tile): enough that a batch of
-// any size puts about four on every compute unit, as long as each keeps
-// kMinTiles steps when every page of the table is in use.  A sequence shorter
-// than that is cut into as many equal parts (split_tiles).
+// Parts that one (sequence, kv head, head tile) is split into at most: four
+// workgroups a compute unit when every page of the table is in use, eight
+// where several sequences may differ in length, as long as each part keeps
+// kMinTiles steps.  A shorter sequence takes parts of the same size, kFullTiles
+// at most, and then fewer of them (split_tiles).  Measured on 32 sequences of
+// 1000 to 8192 positions with 8 kv heads of 128, 16 to a page: 8 a unit
+// 116 us, 4 a unit 120 us; one sequence of 131001: 104 and 100.5 us.
 int attn_nsplit(int64_t n_seqs, int H, int Hkv, int64_t max_pages, int page) {
   const int64_t rows = std::max<int64_t>(n_seqs * Hkv * head_tiles_of(H / Hkv), 1);
   const int64_t tiles = (max_pages * page + kKeys - 1) / kKeys;
-  const int64_t want = (4 * int64_t(device_cu_count()) + rows - 1) / rows;
+  const int64_t want = ((n_seqs > 1 ? 8 : 4) * int64_t(device_cu_count()) + rows - 1) / rows;
   return int(std::max<int64_t>(1, std::min<int64_t>({want, tiles / kMinTiles, kMaxSplit})));
 }
 
@@ -422,6 +437,8 @@ aa_status_t launch_attn_decode(const AttnCall& c, hipStream_t stream) {
   p.head_tiles = head_tiles_of(p.G);
   p.page_shift = page_shift_of(c.page_size);
   p.nsplit = attn_nsplit(c.n_seqs, c.n_heads, c.n_kv_heads, c.max_pages, c.page_size);
+  const int64_t tiles = (c.max_pages * c.page_size + kKeys - 1) / kKeys;
+  p.min_tiles = int(std::min<int64_t>(std::max<int64_t>(tiles / p.nsplit, kMinTiles), kFullTiles));
   p.o_f32 = c.o_dtype == AA_F32;
   p.scale = c.scale;
   p.part = static_cast<float*>(c.workspace);
