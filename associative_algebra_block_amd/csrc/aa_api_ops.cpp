@@ -23,7 +23,7 @@ aa_status_t check_norm(int64_t M, int64_t d, const char* fn) {
   if (M < 0) return fail(AA_ERR_INVALID_ARG, std::string(fn) + ": M is negative");
   if (M >= (int64_t(1) << 31)) return fail(AA_ERR_UNSUPPORTED, std::string(fn) + ": M of 2^31 rows or more");
   if (d < 1) return fail(AA_ERR_INVALID_ARG, std::string(fn) + ": d is less than 1");
-  if (d > aa::kNormMaxWidth) return fail(AA_ERR_UNSUPPORTED, std::string(fn) + ": rows wider than 32768 features");
+  if (d > aa::kNormMaxWidth) return fail(AA_ERR_UNSUPPORTED, std::string(fn) + ": rows wider than 16384 features");
   return AA_OK;
 }
 

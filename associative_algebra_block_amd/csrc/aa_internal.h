@@ -120,7 +120,7 @@ struct NormBwdCall {
   aa_dtype_t x_dtype, dy_dtype;
   float* workspace;
 };
-constexpr int64_t kNormMaxWidth = 32768;
+constexpr int64_t kNormMaxWidth = 16384;
 aa_status_t launch_norm_fwd(const NormFwdCall& call, hipStream_t stream);
 size_t norm_bwd_workspace_bytes(int64_t M, int64_t d);
 aa_status_t launch_norm_bwd(const NormBwdCall& call, hipStream_t stream);

@@ -33,32 +33,83 @@ template <typename T> struct Vec4;
 template <> struct Vec4<float> { typedef f32x4_u type; };
 template <> struct Vec4<__bf16> { typedef bf16x4_u type; };
 
-// v[0..3] = p[0..3], of which only the first n exist (the rest are zero).
-template <typename T>
-__device__ inline void load_chunk(const T* p, int64_t n, float* v) {
-  if (n >= kVec) {
-    const typename Vec4<T>::type t = *reinterpret_cast<const typename Vec4<T>::type*>(p);
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) v[e] = float(t[e]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) v[e] = e < n ? float(p[e]) : 0.0f;
-  }
-}
+// Where a lane's features lie in a row: NC chunks of four, a row's lanes after
+// one another, and behind the last whole chunk up to three features, one for
+// each of the row's first lanes.
+struct Place {
+  int lane, lanes;   // of the row
+  int whole, d;      // features in whole chunks, all features
+  __device__ int col(int c) const { return (c * lanes + lane) * kVec; }
+  __device__ bool has(int c) const { return col(c) < whole; }
+  __device__ bool has_tail() const { return lane < d - whole; }
+};
 
-template <typename T>
-__device__ inline void store_chunk(T* p, int64_t n, const float* v) {
-  if (n >= kVec) {
-    typename Vec4<T>::type t;
+// A lane's part of a row as it lies in memory: the loads go out together, and
+// nothing is converted before all of them are on their way.
+template <typename T, int NC>
+struct RawRow {
+  typename Vec4<T>::type v[NC];
+  T tail;
+  __device__ void load(const T* row, const Place& at) {
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) t[e] = T(v[e]);
-    *reinterpret_cast<typename Vec4<T>::type*>(p) = t;
-  } else {
-#pragma unroll
-    for (int e = 0; e < kVec; ++e)
-      if (e < n) p[e] = T(v[e]);
+    for (int c = 0; c < NC; ++c) {
+      v[c] = typename Vec4<T>::type{T(0.0f), T(0.0f), T(0.0f), T(0.0f)};
+      if (at.has(c)) v[c] = *reinterpret_cast<const typename Vec4<T>::type*>(row + at.col(c));
+    }
+    tail = T(0.0f);
+    if (at.has_tail()) tail = row[at.whole + at.lane];
   }
-}
+};
+
+// The same in float32; features that the lane does not have are zero.
+template <int NC>
+struct Row {
+  float v[NC][kVec], tail;
+  template <typename T>
+  __device__ void set(const RawRow<T, NC>& r) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) v[c][e] = float(r.v[c][e]);
+    tail = float(r.tail);
+  }
+  template <typename T>
+  __device__ void load(const T* row, const Place& at) {
+    RawRow<T, NC> r;
+    r.load(row, at);
+    set(r);
+  }
+  __device__ void fill(float x) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) v[c][e] = x;
+    tail = x;
+  }
+  template <typename T>
+  __device__ void store(T* row, const Place& at) const {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+      if (at.has(c)) {
+        typename Vec4<T>::type t;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) t[e] = T(v[c][e]);
+        *reinterpret_cast<typename Vec4<T>::type*>(row + at.col(c)) = t;
+      }
+    if (at.has_tail()) row[at.whole + at.lane] = T(tail);
+  }
+  // f(chunk, element) -> void over all of a lane's features; chunk NC is the tail
+  template <typename F>
+  __device__ static void each(F f) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) f(c, e);
+    f(NC, 0);
+  }
+  __device__ float& operator()(int c, int e) { return c < NC ? v[c][e] : tail; }
+  __device__ float operator()(int c, int e) const { return c < NC ? v[c][e] : tail; }
+};
 
 __device__ inline float wave_sum(float v) {
 #pragma unroll
@@ -103,58 +154,47 @@ template <typename TX, typename TY, int WPR, int NC>
 __global__ __launch_bounds__(WPR == 1 ? 256 : WPR * 64) void norm_fwd_kernel(NormFwdParams p) {
   constexpr int kRowsPerWg = WPR == 1 ? 4 : 1;
   __shared__ float slots[2 * WPR];
-  const int wave = threadIdx.x / kWave;
-  const int lane_in_row = WPR == 1 ? threadIdx.x & (kWave - 1) : threadIdx.x;
-  const float d = float(p.d);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);   // uniform: row addresses stay scalar
+  const Place at = {int(WPR == 1 ? threadIdx.x & (kWave - 1) : threadIdx.x), 64 * WPR, int(p.d) & ~(kVec - 1),
+                    int(p.d)};
+  const float d = float(at.d);
   for (int64_t row = int64_t(blockIdx.x) * kRowsPerWg + (WPR == 1 ? wave : 0); row < p.M;
        row += int64_t(gridDim.x) * kRowsPerWg) {
     const int64_t base = row * p.d;
-    float x[NC][kVec];
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int64_t col = int64_t(c * 64 * WPR + lane_in_row) * kVec;
-      load_chunk(static_cast<const TX*>(p.X) + base + col, p.d - col, x[c]);
-    }
+    Row<NC> x;
     if (p.delta) {
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int64_t col = int64_t(c * 64 * WPR + lane_in_row) * kVec;
-        float t[kVec];
-        if (p.delta_f32) load_chunk(static_cast<const float*>(p.delta) + base + col, p.d - col, t);
-        else load_chunk(static_cast<const __bf16*>(p.delta) + base + col, p.d - col, t);
-        // the norm is that of the stored sum (rounded to x's type): the
-        // backward pass reads it from S
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) x[c][e] = float(TX(x[c][e] + t[e]));
-        store_chunk(static_cast<TX*>(p.S) + base + col, p.d - col, x[c]);
-      }
+      // the norm is that of the stored sum (rounded to x's type): the
+      // backward pass reads it from S
+      RawRow<TX, NC> rx;
+      rx.load(static_cast<const TX*>(p.X) + base, at);
+      Row<NC> t;
+      if (p.delta_f32) t.load(static_cast<const float*>(p.delta) + base, at);
+      else t.load(static_cast<const __bf16*>(p.delta) + base, at);
+      x.set(rx);
+      Row<NC>::each([&](int c, int e) { x(c, e) = float(TX(x(c, e) + t(c, e))); });
+      x.store(static_cast<TX*>(p.S) + base, at);
+    } else {
+      x.load(static_cast<const TX*>(p.X) + base, at);
     }
     float sum = 0.0f;
 #pragma unroll
-    for (int c = 0; c < NC; ++c) sum += (x[c][0] + x[c][1]) + (x[c][2] + x[c][3]);
-    const float mean = row_sum<WPR>(sum, slots) / d;
+    for (int c = 0; c < NC; ++c) sum += (x.v[c][0] + x.v[c][1]) + (x.v[c][2] + x.v[c][3]);
+    const float mean = row_sum<WPR>(sum + x.tail, slots) / d;
     float sq = 0.0f;
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int64_t col = int64_t(c * 64 * WPR + lane_in_row) * kVec;
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        x[c][e] -= mean;
-        sq += col + e < p.d ? x[c][e] * x[c][e] : 0.0f;
-      }
-    }
+    Row<NC>::each([&](int c, int e) {
+      const bool mine = c < NC ? at.has(c) : at.has_tail();
+      x(c, e) = mine ? x(c, e) - mean : 0.0f;
+      sq += x(c, e) * x(c, e);
+    });
     const float rstd = 1.0f / sqrtf(row_sum<WPR>(sq, slots + WPR) / d + p.eps);
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int64_t col = int64_t(c * 64 * WPR + lane_in_row) * kVec;
-      float g[kVec] = {1.0f, 1.0f, 1.0f, 1.0f}, b[kVec] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (p.gamma) load_chunk(p.gamma + col, p.d - col, g);
-      if (p.beta) load_chunk(p.beta + col, p.d - col, b);
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) x[c][e] = x[c][e] * rstd * g[e] + b[e];
-      store_chunk(static_cast<TY*>(p.Y) + base + col, p.d - col, x[c]);
-    }
-    if (p.mean && lane_in_row == 0) {
+    Row<NC> g, b;
+    g.fill(1.0f);
+    b.fill(0.0f);
+    if (p.gamma) g.load(p.gamma, at);
+    if (p.beta) b.load(p.beta, at);
+    Row<NC>::each([&](int c, int e) { x(c, e) = x(c, e) * rstd * g(c, e) + b(c, e); });
+    x.store(static_cast<TY*>(p.Y) + base, at);
+    if (p.mean && at.lane == 0) {
       p.mean[row] = mean;
       p.rstd[row] = rstd;
     }
@@ -173,131 +213,127 @@ struct NormBwdParams {
   int64_t M, d;
 };
 
-// Same split as the forward kernel.  A wave meets the same features in every
-// row, so the weights' gradients gather in its registers; the waves of a
-// workgroup add theirs in order through LDS and the workgroup writes one
-// partial row, which norm_bwd_reduce_kernel sums: no atomics, so the result
-// does not depend on the order of execution.
+// Same split as the forward kernel, with kBwdWaves rows a workgroup at one wave
+// a row.  A wave meets the same features in every row, so the weights'
+// gradients gather in its registers; the waves of a workgroup add theirs in
+// order through LDS and the workgroup writes one partial row, which
+// norm_bwd_reduce_kernel sums: no atomics, so the result does not depend on the
+// order of execution.
+constexpr int kBwdWaves = 4;
 template <typename TX, typename TY, int WPR, int NC>
-__global__ __launch_bounds__(WPR == 1 ? 256 : WPR * 64) void norm_bwd_kernel(NormBwdParams p) {
-  constexpr int kRowsPerWg = WPR == 1 ? 4 : 1;
+__global__ __launch_bounds__(WPR == 1 ? kBwdWaves * 64 : WPR * 64, WPR == 1 && NC <= 3 ? 4 : 1) void norm_bwd_kernel(NormBwdParams p) {
+  constexpr int kRowsPerWg = WPR == 1 ? kBwdWaves : 1;
   __shared__ float slots[2 * WPR];
   extern __shared__ float sums[];   // WPR == 1: [2][d]
-  const int wave = threadIdx.x / kWave;
-  const int lane_in_row = WPR == 1 ? threadIdx.x & (kWave - 1) : threadIdx.x;
-  const float d = float(p.d);
-  float dg[NC][kVec], db[NC][kVec];
-#pragma unroll
-  for (int c = 0; c < NC; ++c)
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) dg[c][e] = db[c][e] = 0.0f;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);   // uniform: row addresses stay scalar
+  const Place at = {int(WPR == 1 ? threadIdx.x & (kWave - 1) : threadIdx.x), 64 * WPR, int(p.d) & ~(kVec - 1),
+                    int(p.d)};
+  const float d = float(at.d);
+  Row<NC> dg, db;
+  dg.fill(0.0f);
+  db.fill(0.0f);
   for (int64_t row = int64_t(blockIdx.x) * kRowsPerWg + (WPR == 1 ? wave : 0); row < p.M;
        row += int64_t(gridDim.x) * kRowsPerWg) {
-    const int64_t base = row * p.d;
+    RawRow<TX, NC> rx, rs;
+    RawRow<TY, NC> ry;
+    Row<NC> xh, g, gm;
+    rx.load(static_cast<const TX*>(p.X) + row * p.d, at);
+    ry.load(static_cast<const TY*>(p.dY) + row * p.d, at);
     const float mean = p.mean[row], rstd = p.rstd[row];
-    float xh[NC][kVec], g[NC][kVec];
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int64_t col = int64_t(c * 64 * WPR + lane_in_row) * kVec;
-      load_chunk(static_cast<const TX*>(p.X) + base + col, p.d - col, xh[c]);
-      load_chunk(static_cast<const TY*>(p.dY) + base + col, p.d - col, g[c]);
-    }
+    gm.fill(1.0f);
+    if (p.gamma) gm.load(p.gamma, at);
+    if (p.dS) rs.load(static_cast<const TX*>(p.dS) + row * p.d, at);   // needed last
+    xh.set(rx);
+    g.set(ry);
     float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int64_t col = int64_t(c * 64 * WPR + lane_in_row) * kVec;
-      float gm[kVec] = {1.0f, 1.0f, 1.0f, 1.0f};
-      if (p.gamma) load_chunk(p.gamma + col, p.d - col, gm);
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) {
-        // behind the row's end dy is zero, so xh only has to be finite there
-        xh[c][e] = col + e < p.d ? (xh[c][e] - mean) * rstd : 0.0f;
-        dg[c][e] += g[c][e] * xh[c][e];
-        db[c][e] += g[c][e];
-        g[c][e] *= gm[e];
-        s1 += g[c][e];
-        s2 += g[c][e] * xh[c][e];
-      }
-    }
+    Row<NC>::each([&](int c, int e) {
+      // features that are not there have dy = 0; xh only has to be finite
+      const bool mine = c < NC ? at.has(c) : at.has_tail();
+      xh(c, e) = mine ? (xh(c, e) - mean) * rstd : 0.0f;
+      dg(c, e) += g(c, e) * xh(c, e);
+      db(c, e) += g(c, e);
+      g(c, e) *= gm(c, e);
+      s1 += g(c, e);
+      s2 += g(c, e) * xh(c, e);
+    });
     s1 = row_sum<WPR>(s1, slots) / d;
     s2 = row_sum<WPR>(s2, slots + WPR) / d;
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int64_t col = int64_t(c * 64 * WPR + lane_in_row) * kVec;
-      float r[kVec] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (p.dS) load_chunk(static_cast<const TX*>(p.dS) + base + col, p.d - col, r);
-#pragma unroll
-      for (int e = 0; e < kVec; ++e) r[e] += rstd * (g[c][e] - s1 - xh[c][e] * s2);
-      store_chunk(static_cast<TX*>(p.dX) + base + col, p.d - col, r);
-    }
+    Row<NC> res;
+    res.fill(0.0f);
+    if (p.dS) res.set(rs);
+    Row<NC>::each([&](int c, int e) { res(c, e) += rstd * (g(c, e) - s1 - xh(c, e) * s2); });
+    res.store(static_cast<TX*>(p.dX) + row * p.d, at);
   }
   if (!p.part) return;
   float* out = p.part + int64_t(blockIdx.x) * 2 * p.d;
   if constexpr (WPR == 1) {
-    for (int w = 0; w < 4; ++w) {
+    for (int w = 0; w < kBwdWaves; ++w) {
       if (wave == w) {
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const int64_t col = int64_t(c * 64 + lane_in_row) * kVec;
-#pragma unroll
-          for (int e = 0; e < kVec; ++e) {
-            if (col + e >= p.d) break;
-            sums[col + e] = (w ? sums[col + e] : 0.0f) + dg[c][e];
-            sums[p.d + col + e] = (w ? sums[p.d + col + e] : 0.0f) + db[c][e];
+        Row<NC>::each([&](int c, int e) {
+          const bool mine = c < NC ? at.has(c) : at.has_tail();
+          const int col = c < NC ? at.col(c) + e : at.whole + at.lane;
+          if (mine) {
+            sums[col] = (w ? sums[col] : 0.0f) + dg(c, e);
+            sums[at.d + col] = (w ? sums[at.d + col] : 0.0f) + db(c, e);
           }
-        }
+        });
       }
       __syncthreads();
     }
-    for (int64_t i = threadIdx.x; i < 2 * p.d; i += blockDim.x) out[i] = sums[i];
+    for (int i = threadIdx.x; i < 2 * at.d; i += blockDim.x) out[i] = sums[i];
   } else {
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      const int64_t col = int64_t(c * 64 * WPR + lane_in_row) * kVec;
-      store_chunk(out + col, p.d - col, dg[c]);
-      store_chunk(out + p.d + col, p.d - col, db[c]);
-    }
+    dg.store(out, at);
+    db.store(out + p.d, at);
   }
 }
 
-// dgamma, dbeta = sums of the G partial rows; 64 columns a workgroup, its 16
-// waves take the rows in turn and join in LDS, in a fixed order.
+// dgamma, dbeta = sums of the G partial rows.  A workgroup takes 16 columns, so
+// that 768 features give 96 workgroups: its 64 groups of 16 lanes take the rows
+// in turn and join in LDS, in a fixed order.
+constexpr int kCols = 16, kRowGroups = 1024 / kCols;
 __global__ __launch_bounds__(1024) void norm_bwd_reduce_kernel(const float* part, int G, int64_t d, float* dgamma,
                                                                float* dbeta) {
-  __shared__ float red[16][kWave];
-  const int wave = threadIdx.x / kWave, lane = threadIdx.x & (kWave - 1);
-  const int64_t col = int64_t(blockIdx.x) * kWave + lane;   // of 2 d
+  __shared__ float red[kRowGroups][kCols];
+  const int c = threadIdx.x % kCols, group = threadIdx.x / kCols;
+  const int64_t col = int64_t(blockIdx.x) * kCols + c;   // of 2 d
   float acc = 0.0f;
   if (col < 2 * d) {
-#pragma unroll 4
-    for (int g = wave; g < G; g += 16) acc += part[int64_t(g) * 2 * d + col];
+#pragma unroll 8
+    for (int g = group; g < G; g += kRowGroups) acc += part[int64_t(g) * 2 * d + col];
   }
-  red[wave][lane] = acc;
+  red[group][c] = acc;
   __syncthreads();
-  if (wave == 0 && col < 2 * d) {
+  if (threadIdx.x < kWave) {   // four partial columns a lane column
+    acc = 0.0f;
 #pragma unroll
-    for (int w = 1; w < 16; ++w) acc += red[w][lane];
+    for (int g = 0; g < kRowGroups / 4; ++g) acc += red[group * (kRowGroups / 4) + g][c];
+    acc += __shfl_xor(acc, kCols, kWave);
+    acc += __shfl_xor(acc, 2 * kCols, kWave);
     float* out = col < d ? dgamma : dbeta;
-    if (out) out[col < d ? col : col - d] = acc;
+    if (group == 0 && col < 2 * d && out) out[col < d ? col : col - d] = acc;
   }
 }
 
-// Rows are dealt to at most this many workgroups of 256 threads (or 4 times
-// fewer of 1024).
+// Rows are dealt to at most 16 workgroups a compute unit.  With half as many,
+// which still fill it, the rows of a wave follow one another and the second
+// one's loads wait for the first one's stores: 30.5 against 27.9 us for 12288
+// rows of 768.
 int64_t fwd_grid(int64_t M, int wpr) {
   const int64_t rows_per_wg = wpr == 1 ? 4 : 1;
   const int64_t wgs = (M + rows_per_wg - 1) / rows_per_wg;
-  const int64_t cap = int64_t(device_cu_count()) * (wpr == 16 ? 2 : 8);
-  if (wgs <= cap) return wgs;
+  const int64_t cap = int64_t(device_cu_count()) * 16;
   const int64_t rounds = (wgs + cap - 1) / cap;   // every workgroup the same number of rows
   return (wgs + rounds - 1) / rounds;
 }
 
-constexpr int kBwdMaxGrid = 512;
+// Workgroups of the backward kernel, each of which writes 2 d partial sums.
+// Narrow rows: what fits the chip at once (1024 of 4 waves; 512 of 8 waves, as
+// many rows in flight, took 38 against 30 us for 12288 rows of 768).  Wider
+// ones: fewer, so that the partial sums stay a small part of the traffic.
 int64_t bwd_grid(int64_t M, int64_t d) {
-  const int64_t rows_per_wg = d <= 2048 ? 4 : 1;
+  const int64_t rows_per_wg = d <= 1024 ? kBwdWaves : 1, cap = d <= 1024 ? 1024 : d <= 2048 ? 512 : 256;
   const int64_t wgs = (M + rows_per_wg - 1) / rows_per_wg;
-  const int64_t rounds = (wgs + kBwdMaxGrid - 1) / kBwdMaxGrid;
+  const int64_t rounds = (wgs + cap - 1) / cap;
   return rounds ? (wgs + rounds - 1) / rounds : 0;
 }
 
@@ -308,10 +344,10 @@ int64_t bwd_grid(int64_t M, int64_t d) {
     else if ((d) <= 512) CALL(1, 2);    \
     else if ((d) <= 768) CALL(1, 3);    \
     else if ((d) <= 1024) CALL(1, 4);   \
-    else if ((d) <= 2048) CALL(1, 8);   \
+    else if ((d) <= 2048) CALL(4, 2);   \
     else if ((d) <= 4096) CALL(4, 4);   \
     else if ((d) <= 8192) CALL(4, 8);   \
-    else CALL(16, 8);                   \
+    else CALL(8, 8);                    \
   } while (0)
 
 template <typename TX, typename TY>
@@ -327,7 +363,7 @@ template <typename TX, typename TY>
 void launch_bwd(const NormBwdParams& p, hipStream_t stream) {
   const uint32_t grid = uint32_t(bwd_grid(p.M, p.d));
 #define AA_CALL(WPR, NC)                                                                              \
-  launch((norm_bwd_kernel<TX, TY, WPR, NC>), dim3(grid), dim3(WPR == 1 ? 256 : WPR * 64),             \
+  launch((norm_bwd_kernel<TX, TY, WPR, NC>), dim3(grid), dim3(WPR == 1 ? kBwdWaves * 64 : WPR * 64),  \
          uint32_t(WPR == 1 && p.part ? 8 * p.d : 0), stream, p)
   AA_NORM_SPLIT(p.d, AA_CALL);
 #undef AA_CALL
@@ -365,7 +401,7 @@ aa_status_t launch_norm_bwd(const NormBwdCall& c, hipStream_t stream) {
     if (st != AA_OK || !sums) return st;
   }
   if (!sums) return AA_OK;
-  launch(norm_bwd_reduce_kernel, dim3(uint32_t((2 * c.d + kWave - 1) / kWave)), dim3(1024), 0u, stream,
+  launch(norm_bwd_reduce_kernel, dim3(uint32_t((2 * c.d + kCols - 1) / kCols)), dim3(1024), 0u, stream,
          static_cast<const float*>(c.workspace), int(bwd_grid(c.M, c.d)), c.d, c.dgamma, c.dbeta);
   return after_launch(stream, "norm_bwd_reduce_kernel");
 }

@@ -255,7 +255,7 @@ aa_status_t aa_project_bwd_weight(aa_plan_t plan, const void* X, const void* dY,
  * given exactly when delta is and equal to X to add in place; gamma and beta
  * are d float32 values or NULL (ones, zeros); mean and rstd receive mu and r
  * (M float32 each) for the backward pass, or are both NULL.  Y must not
- * overlap another operand.  1 <= d <= 32768, any width and row count; sums and
+ * overlap another operand.  1 <= d <= 16384, any width and row count; sums and
  * statistics are float32, the variance that of the deviations from the mean.
  * M == 0 is a no-op. */
 aa_status_t aa_layernorm_fwd(const void* X, const void* delta, const float* gamma, const float* beta, void* S,

@@ -37,9 +37,9 @@ int main() {
   float *g = P<float>(3), *b = P<float>(4), *mu = P<float>(7), *r = P<float>(8);
   const int64_t big = (int64_t(1) << 31) - 1;
   EXPECT(aa_layernorm_fwd(P(1), P(2), g, b, P(5), P(6), mu, r, 8, 768, 1e-5f, AA_F32, AA_BF16, AA_BF16, nullptr), AA_OK, 1);
-  EXPECT(aa_layernorm_fwd(P(1), P(2), g, b, P(1), P(600), mu, r, big, 32768, 0.0f, AA_BF16, AA_BF16, AA_F32, nullptr),
+  EXPECT(aa_layernorm_fwd(P(1), P(2), g, b, P(1), P(600), mu, r, big, 16384, 0.0f, AA_BF16, AA_BF16, AA_F32, nullptr),
          AA_ERR_INVALID_ARG, 0);   // rows so many that X runs into the others
-  EXPECT(aa_layernorm_fwd(P(1), nullptr, nullptr, nullptr, nullptr, P(600), nullptr, nullptr, big, 32768, 0.0f, AA_F32,
+  EXPECT(aa_layernorm_fwd(P(1), nullptr, nullptr, nullptr, nullptr, P(600), nullptr, nullptr, big, 16384, 0.0f, AA_F32,
                           AA_F32, AA_F32, nullptr), AA_OK, 1);
   EXPECT(aa_layernorm_fwd(P(1), nullptr, g, b, P(5), P(6), mu, r, 8, 768, 1e-5f, AA_F32, AA_BF16, AA_BF16, nullptr),
          AA_ERR_INVALID_ARG, 0);

@@ -33,7 +33,7 @@ NORM = dict(X=G, delta=2 * G, gamma=3 * G, beta=4 * G, S=5 * G, Y=6 * G, mean=7 
 
 
 @pytest.mark.parametrize("status,changed", [
-    (BAD, dict(M=-1)), (BAD, dict(d=0)), (BAD, dict(d=-3)), (UNSUP, dict(d=32769)), (UNSUP, dict(M=1 << 31)),
+    (BAD, dict(M=-1)), (BAD, dict(d=0)), (BAD, dict(d=-3)), (UNSUP, dict(d=16385)), (UNSUP, dict(M=1 << 31)),
     (BAD, dict(eps=-1e-5)), (BAD, dict(eps=float("nan"))), (BAD, dict(eps=float("inf"))),
     (BAD, dict(xt=2)), (BAD, dict(dt=-1)), (BAD, dict(yt=7)),
     (BAD, dict(X=None)), (BAD, dict(Y=None)), (BAD, dict(X=G + 8)), (BAD, dict(Y=6 * G + 2)), (BAD, dict(gamma=3 * G + 4)),
