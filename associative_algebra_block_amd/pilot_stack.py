@@ -25,6 +25,11 @@ a KV cache, the LM head, argmax) is plain torch, identical in both models.
 Attention runs in float32 (scores and cache); the projections take bf16
 operands, as the FFN does.
 
+With ops="library" the LayerNorms (with the residual adds before them), the KV
+cache and the attention of the decode steps are the library's too
+(aa_layernorm_fwd, aa_kv_append, aa_attn_decode): the cache is paged and in
+bf16, the residual stream, scores and softmax stay float32.
+
 One decode step advances every sequence of the batch by one token at the
 position held in a device tensor, so a step can be captured in a HIP graph
 and replayed for any position: the algebra FFN takes the row types from a
@@ -37,7 +42,11 @@ from dataclasses import dataclass
 
 import torch
 
-from . import aa_plan_create, aa_swiglu_ffn_fwd, pack
+from . import (aa_attn_decode, aa_attn_decode_workspace, aa_kv_append, aa_layernorm_fwd, aa_plan_create,
+               aa_swiglu_ffn_fwd, pack)
+
+
+PAGE = 64   # positions of a page of the library's KV cache
 
 
 @dataclass(frozen=True)
@@ -95,10 +104,12 @@ class PilotGenerator:
     advances all B sequences by one position (device-side position, so the
     step can be captured in a HIP graph)."""
 
-    def __init__(self, cfg: PilotConfig, weights: dict, ffn: str, batch: int, dev, argmax_in_step=True):
+    def __init__(self, cfg: PilotConfig, weights: dict, ffn: str, batch: int, dev, argmax_in_step=True, ops="torch"):
         if ffn not in ("algebra", "dense"):
             raise ValueError("ffn must be 'algebra' or 'dense'")
-        self.cfg, self.w, self.ffn, self.B, self.dev = cfg, weights, ffn, batch, dev
+        if ops not in ("torch", "library"):
+            raise ValueError("ops must be 'torch' or 'library'")
+        self.cfg, self.w, self.ffn, self.B, self.dev, self.ops = cfg, weights, ffn, batch, dev, ops
         self.argmax_in_step = argmax_in_step
         # when a list: every FFN call appends (layer, FFN input, FFN output,
         # prompt length of a prefill or 0, the decode row types or None);
@@ -106,10 +117,22 @@ class PilotGenerator:
         self.trace = None
         H, hd, L = cfg.heads, cfg.d // cfg.heads, cfg.layers
         self.hd = hd
-        # K cache stored transposed (head dim before position) so that q K^T is
-        # a product with a contiguous right operand
-        self.Kt = torch.zeros(L, batch * H, hd, cfg.ctx, device=dev)
-        self.V = torch.zeros(L, batch * H, cfg.ctx, hd, device=dev)
+        if ops == "library":
+            # every sequence's pages one after the other; the layers share the table
+            per = -(-cfg.ctx // PAGE)
+            self.Kp = torch.zeros(L, batch * per, H, PAGE, hd, dtype=torch.bfloat16, device=dev)
+            self.Vp = torch.zeros(L, batch * per, H, hd, PAGE, dtype=torch.bfloat16, device=dev)
+            self.table = torch.arange(batch * per, dtype=torch.int32, device=dev).view(batch, per)
+            self.pos32 = torch.zeros(batch, dtype=torch.int32, device=dev)
+            self.lens = torch.zeros(batch, dtype=torch.int32, device=dev)
+            self.attn_ws = torch.empty(max(aa_attn_decode_workspace(batch, H, H, hd, PAGE, per), 16),
+                                       dtype=torch.uint8, device=dev)
+            self.o = torch.empty(batch, H, hd, dtype=torch.bfloat16, device=dev)
+        else:
+            # K cache stored transposed (head dim before position) so that q K^T
+            # is a product with a contiguous right operand
+            self.Kt = torch.zeros(L, batch * H, hd, cfg.ctx, device=dev)
+            self.V = torch.zeros(L, batch * H, cfg.ctx, hd, device=dev)
         self.pos = torch.zeros(1, dtype=torch.int64, device=dev)
         self.token = torch.zeros(batch, dtype=torch.int64, device=dev)
         self.types = torch.zeros(batch, dtype=torch.int32, device=dev)
@@ -161,6 +184,12 @@ class PilotGenerator:
     def _ln(self, x, wt, b):
         return torch.nn.functional.layer_norm(x, (self.cfg.d,), wt, b, 1e-5)
 
+    def _add_ln(self, x, delta, wt, b, dtype=torch.bfloat16):
+        """The library's norm of x + delta, which replaces x (None: of x)."""
+        y = torch.empty(x.shape, dtype=dtype, device=self.dev)
+        aa_layernorm_fwd(x, wt, b, y, delta, None if delta is None else x, eps=1e-5)
+        return y
+
     def _qkv(self, lw, a_bf16):
         return torch.matmul(a_bf16, lw["Wqkv"]).float() + lw["bqkv"]
 
@@ -177,22 +206,41 @@ class PilotGenerator:
         M = B * P
         x = self.w["E"][tokens.reshape(-1)].float() + self.w["P"][:P].repeat(B, 1)   # [M, d]
         causal = torch.triu(torch.full((P, P), float("-inf"), device=self.dev), diagonal=1)
+        library = self.ops == "library"
+        if library:
+            seq = torch.arange(B, dtype=torch.int32, device=self.dev).repeat_interleave(P)
+            place = torch.arange(P, dtype=torch.int32, device=self.dev).repeat(B)
+        y = None
         for l, lw in enumerate(self.w["layers"]):
-            a = self._ln(x, lw["ln1_w"], lw["ln1_b"]).to(torch.bfloat16)
+            if library:
+                a = self._add_ln(x, y, lw["ln1_w"], lw["ln1_b"])
+            else:
+                a = self._ln(x, lw["ln1_w"], lw["ln1_b"]).to(torch.bfloat16)
             qkv = self._qkv(lw, a).view(B, P, 3, Hh, hd)
             q = qkv[:, :, 0].permute(0, 2, 1, 3).reshape(B * Hh, P, hd)
             k = qkv[:, :, 1].permute(0, 2, 1, 3).reshape(B * Hh, P, hd)
             v = qkv[:, :, 2].permute(0, 2, 1, 3).reshape(B * Hh, P, hd).contiguous()
             kt = k.transpose(1, 2).contiguous()
-            self.Kt[l, :, :, :P] = kt
-            self.V[l, :, :P] = v
+            if library:
+                rows = qkv.view(M, 3 * d)
+                aa_kv_append(rows[:, d:2 * d], rows[:, 2 * d:], self.Kp[l], self.Vp[l], self.table, place, seq)
+            else:
+                self.Kt[l, :, :, :P] = kt
+                self.V[l, :, :P] = v
             s = torch.bmm(q.contiguous(), kt) * (1.0 / math.sqrt(hd)) + causal
             o = torch.bmm(torch.softmax(s, dim=-1), v)                       # [B H, P, hd]
             o = o.view(B, Hh, P, hd).permute(0, 2, 1, 3).reshape(M, d)
+            if library:
+                att = torch.matmul(o.to(torch.bfloat16), lw["Wo"]).float() + lw["bo"]
+                y = self._ffn(l, self._add_ln(x, att, lw["ln2_w"], lw["ln2_b"]), prefill_len=P)
+                continue
             x = x + torch.matmul(o.to(torch.bfloat16), lw["Wo"]).float() + lw["bo"]
             f = self._ln(x, lw["ln2_w"], lw["ln2_b"]).to(torch.bfloat16)
             x = x + self._ffn(l, f, prefill_len=P)
-        hf = self._ln(x, self.w["lnf_w"], self.w["lnf_b"])
+        if library:
+            hf = self._add_ln(x, y, self.w["lnf_w"], self.w["lnf_b"], torch.float32)
+        else:
+            hf = self._ln(x, self.w["lnf_w"], self.w["lnf_b"])
         last = hf.view(B, P, d)[:, -1].to(torch.bfloat16)
         self.logits.copy_(torch.matmul(last, self.w["E_T"]))
         self.token.copy_(torch.argmax(self.logits, dim=-1))
@@ -206,10 +254,38 @@ class PilotGenerator:
         logits, the next token (argmax) and advance the position.  Reads the
         position only from device memory."""
         cfg, B = self.cfg, self.B
-        Hh, hd, d = cfg.heads, self.hd, cfg.d
         pos = self.pos
         self.types.copy_(torch.remainder(pos, cfg.q).to(torch.int32).expand(B))
         x = torch.index_select(self.w["E"], 0, self.token).float() + torch.index_select(self.w["P"], 0, pos)
+        if self.ops == "library":
+            hf = self._decode_layers(x)
+        else:
+            hf = self._decode_layers_torch(x)
+        self.hidden.copy_(hf)
+        self.logits.copy_(torch.matmul(hf.to(torch.bfloat16), self.w["E_T"]))
+        if self.argmax_in_step:
+            self.pick()
+        pos.add_(1)
+
+    def _decode_layers(self, x):
+        """The layers of a decode step on the residual stream x [B, d] with the
+        library's norms, cache and attention; the final norm's output."""
+        d = self.cfg.d
+        self.pos32.copy_(self.pos.expand(self.B))
+        torch.add(self.pos32, 1, out=self.lens)
+        y = None
+        for l, lw in enumerate(self.w["layers"]):
+            qkv = self._qkv(lw, self._add_ln(x, y, lw["ln1_w"], lw["ln1_b"]))
+            aa_kv_append(qkv[:, d:2 * d], qkv[:, 2 * d:], self.Kp[l], self.Vp[l], self.table, self.pos32)
+            aa_attn_decode(qkv[:, :d], self.Kp[l], self.Vp[l], self.table, self.lens, self.o,
+                           1.0 / math.sqrt(self.hd), self.attn_ws)
+            att = torch.matmul(self.o.view(self.B, d), lw["Wo"]).float() + lw["bo"]
+            y = self._ffn(l, self._add_ln(x, att, lw["ln2_w"], lw["ln2_b"]))
+        return self._add_ln(x, y, self.w["lnf_w"], self.w["lnf_b"], torch.float32)
+
+    def _decode_layers_torch(self, x):
+        cfg, B, pos = self.cfg, self.B, self.pos
+        Hh, hd, d = cfg.heads, self.hd, cfg.d
         keep = self.ar.le(pos)                                         # positions 0 .. pos
         bias = torch.where(keep, 0.0, float("-inf"))                   # [ctx]
         for l, lw in enumerate(self.w["layers"]):
@@ -225,12 +301,7 @@ class PilotGenerator:
             x = x + torch.matmul(o.to(torch.bfloat16), lw["Wo"]).float() + lw["bo"]
             f = self._ln(x, lw["ln2_w"], lw["ln2_b"]).to(torch.bfloat16)
             x = x + self._ffn(l, f)
-        hf = self._ln(x, self.w["lnf_w"], self.w["lnf_b"])
-        self.hidden.copy_(hf)
-        self.logits.copy_(torch.matmul(hf.to(torch.bfloat16), self.w["E_T"]))
-        if self.argmax_in_step:
-            self.pick()
-        pos.add_(1)
+        return self._ln(x, self.w["lnf_w"], self.w["lnf_b"])
 
     def pick(self) -> None:
         """Greedy sampling of the next tokens from the last logits."""

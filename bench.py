@@ -1207,7 +1207,9 @@ def bench_generate(args, torch, aa, dev):
     SwiGLU FFN (torch.matmul) and once with the algebra FFN (Q2 x Q2 through
     aa_swiglu_ffn_fwd), on the same synthetic weights: a 128-token prompt and
     256 new tokens per sequence, batch 1 and batch 8.  Attention over the KV
-    cache, LayerNorms, the LM head and argmax run in torch in both models.
+    cache, LayerNorms, the LM head and argmax run in torch in both models; a
+    third run has the algebra FFN with the library's LayerNorms, paged cache and
+    decode attention (the LM head and argmax in torch).
     value = the algebra model's decode tokens/s at batch 1."""
     from associative_algebra_block_amd.pilot_stack import PilotConfig, PilotGenerator, make_weights
     cfg = PilotConfig()
@@ -1218,10 +1220,10 @@ def bench_generate(args, torch, aa, dev):
         g = torch.Generator(device="cpu")
         g.manual_seed(7 + B)
         prompt = torch.randint(0, cfg.vocab, (B, P), generator=g).to(dev)
-        for ffn in ("dense", "algebra"):
-            gen = PilotGenerator(cfg, w, ffn, B, dev)
+        for ffn, ops in (("dense", "torch"), ("algebra", "torch"), ("algebra", "library")):
+            gen = PilotGenerator(cfg, w, ffn, B, dev, ops=ops)
             pre, dec = generate_timing(torch, gen, prompt, G, reps)
-            runs[(B, ffn)] = {"prefill_ms": round(pre, 4), "decode_ms_per_step": round(dec, 5),
+            runs[(B, ffn if ops == "torch" else "library")] = {"prefill_ms": round(pre, 4), "decode_ms_per_step": round(dec, 5),
                               "decode_tokens_per_s": round(B / (dec * 1e-3), 1),
                               "sequence_tokens_per_s": round(B * G / ((pre + G * dec) * 1e-3), 1)}
             del gen
@@ -1230,6 +1232,7 @@ def bench_generate(args, torch, aa, dev):
     for B in (1, 8):
         d, a = runs[(B, "dense")], runs[(B, "algebra")]
         out[f"batch{B}"] = {"dense_ffn": d, "algebra_ffn": a,
+                            "algebra_ffn_library_norm_and_attention": runs[(B, "library")],
                             "decode_speedup": round(a["decode_tokens_per_s"] / d["decode_tokens_per_s"], 4),
                             "sequence_speedup": round(a["sequence_tokens_per_s"] / d["sequence_tokens_per_s"], 4),
                             "prefill_speedup": round(d["prefill_ms"] / a["prefill_ms"], 4)}
