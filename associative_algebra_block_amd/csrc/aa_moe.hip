@@ -313,34 +313,43 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(MoeParams p) {
   if (live && lane < 16) p.h[pair * p.F + int64_t(k) * bo + strip * 16 + lane] = g / (1.0f + expf(-g)) * u;
 }
 
-// Down projection and weighted sum: a workgroup per 16 output columns of a
-// token.  Its four waves share the parts of the sum over the chosen experts
-// and join in a fixed order.
+// Down projection and weighted sum: a workgroup per NS strips of 16 output
+// columns of a token (NS = 2: neighbours of one output group, which share the
+// loads of the hidden activation; the last of an odd number is alone).  Its
+// four waves share the parts of the sum over the chosen experts and join in a
+// fixed order.
+template <int NS>
 __global__ __launch_bounds__(256) void moe_down_kernel(MoeParams p) {
-  __shared__ float s_part[4][16];
+  __shared__ float s_part[4][NS][16];
   const int64_t t = blockIdx.y;
   const int tau = row_type(p, int(t));
   if (tau < 0 || tau >= p.q) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int bi = int(uint32_t(p.F) / uint32_t(p.q)), bo = int(uint32_t(p.D) / uint32_t(p.q));
-  const int strips = bo / 16;
-  const int k = blockIdx.x / strips, strip = blockIdx.x - k * strips;
+  const int strips = bo / 16, parts = (strips + NS - 1) / NS;
+  const int k = blockIdx.x / parts, strip = (blockIdx.x - k * parts) * NS;
+  const bool both = strip + 1 < strips;
   const Groups groups = leaf_groups_of(p.law, tau, k);
-  const __bf16* W[1] = {p.Wd};
+  const __bf16* W[NS];
+  W[0] = p.Wd;
+  if constexpr (NS == 2) W[1] = p.Wd + (both ? int64_t(bi) * 16 : 0);
   const int32_t* chosen = p.chosen + t * p.top_k;
   const float* weight = p.share + t * p.top_k;
   const int steps = p.top_k * groups.n * ((bi + 31) / 32);
-  float acc[1] = {0.0f};
-  strip_dot<1>(W, [&](int a) { return int64_t(chosen[a]) * p.D * p.F; }, p.h + t * p.top_k * p.F, int(p.F),
-               [&](int a) { return weight[a]; }, groups, k, p.q, bi, int64_t(bi) * bo, strip, lane, wave * steps / 4,
-               (wave + 1) * steps / 4, acc);
-  const float y = quad_sum(acc[0]);
-  if (lane < 16) s_part[wave][lane] = y;
+  float acc[NS] = {};
+  strip_dot<NS>(W, [&](int a) { return int64_t(chosen[a]) * p.D * p.F; }, p.h + t * p.top_k * p.F, int(p.F),
+                [&](int a) { return weight[a]; }, groups, k, p.q, bi, int64_t(bi) * bo, strip, lane, wave * steps / 4,
+                (wave + 1) * steps / 4, acc);
+#pragma unroll
+  for (int i = 0; i < NS; ++i) {
+    const float y = quad_sum(acc[i]);
+    if (lane < 16) s_part[wave][i][lane] = y;
+  }
   __syncthreads();
-  if (threadIdx.x < 16) {
-    const int c = threadIdx.x;
-    const float v = (s_part[0][c] + s_part[1][c]) + (s_part[2][c] + s_part[3][c]);
-    const int64_t at = t * p.D + int64_t(k) * bo + strip * 16 + c;
+  const int i = threadIdx.x / 16, c = threadIdx.x & 15;
+  if (i < NS && strip + i < strips) {
+    const float v = (s_part[0][i][c] + s_part[1][i][c]) + (s_part[2][i][c] + s_part[3][i][c]);
+    const int64_t at = t * p.D + int64_t(k) * bo + (strip + i) * 16 + c;
     if (p.y_f32) static_cast<float*>(p.Y)[at] = v;
     else static_cast<__bf16*>(p.Y)[at] = (__bf16)v;
   }
@@ -405,7 +414,9 @@ aa_status_t launch_moe(const aa_plan_s& up, const aa_plan_s& down, const MoeCall
   else launch((moe_up_kernel<1>), dim3((strips + 7) / 8, pairs), block, lds, stream, p);
   st = after_launch(stream, "moe_up_kernel");
   if (st != AA_OK) return st;
-  launch(moe_down_kernel, dim3(uint32_t(p.D / 16), M), dim3(256), 0u, stream, p);
+  const uint32_t out_strips = uint32_t(p.D / 16), q = uint32_t(p.q);
+  if (M * out_strips < 1024) launch((moe_down_kernel<1>), dim3(out_strips, M), dim3(256), 0u, stream, p);
+  else launch((moe_down_kernel<2>), dim3((out_strips / q + 1) / 2 * q, M), dim3(256), 0u, stream, p);
   return after_launch(stream, "moe_down_kernel");
 }
 

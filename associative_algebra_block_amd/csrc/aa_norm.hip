@@ -223,6 +223,7 @@ constexpr int kBwdWaves = 4;
 template <typename TX, typename TY, int WPR, int NC>
 __global__ __launch_bounds__(WPR == 1 ? kBwdWaves * 64 : WPR * 64, WPR == 1 && NC <= 3 ? 4 : 1) void norm_bwd_kernel(NormBwdParams p) {
   constexpr int kRowsPerWg = WPR == 1 ? kBwdWaves : 1;
+  constexpr bool kAhead = WPR > 1 && NC <= 4;   // the next row is on its way while this one is reduced
   __shared__ float slots[2 * WPR];
   extern __shared__ float sums[];   // WPR == 1: [2][d]
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);   // uniform: row addresses stay scalar
@@ -232,24 +233,34 @@ __global__ __launch_bounds__(WPR == 1 ? kBwdWaves * 64 : WPR * 64, WPR == 1 && N
   Row<NC> dg, db;
   dg.fill(0.0f);
   db.fill(0.0f);
-  for (int64_t row = int64_t(blockIdx.x) * kRowsPerWg + (WPR == 1 ? wave : 0); row < p.M;
-       row += int64_t(gridDim.x) * kRowsPerWg) {
-    RawRow<TX, NC> rx, rs;
-    RawRow<TY, NC> ry;
+  const int64_t step = int64_t(gridDim.x) * kRowsPerWg;
+  int64_t row = int64_t(blockIdx.x) * kRowsPerWg + (WPR == 1 ? wave : 0);
+  RawRow<TX, NC> rx;
+  RawRow<TY, NC> ry;
+  float mean = 0.0f, rstd = 0.0f;
+  auto fetch = [&](int64_t r) {
+    rx.load(static_cast<const TX*>(p.X) + r * p.d, at);
+    ry.load(static_cast<const TY*>(p.dY) + r * p.d, at);
+    mean = p.mean[r];
+    rstd = p.rstd[r];
+  };
+  if (kAhead && row < p.M) fetch(row);
+  for (; row < p.M; row += step) {
+    if (!kAhead) fetch(row);
+    RawRow<TX, NC> rs;
     Row<NC> xh, g, gm;
-    rx.load(static_cast<const TX*>(p.X) + row * p.d, at);
-    ry.load(static_cast<const TY*>(p.dY) + row * p.d, at);
-    const float mean = p.mean[row], rstd = p.rstd[row];
     gm.fill(1.0f);
     if (p.gamma) gm.load(p.gamma, at);
     if (p.dS) rs.load(static_cast<const TX*>(p.dS) + row * p.d, at);   // needed last
     xh.set(rx);
     g.set(ry);
+    const float r_mean = mean, r_rstd = rstd;
+    if (kAhead && row + step < p.M) fetch(row + step);
     float s1 = 0.0f, s2 = 0.0f;
     Row<NC>::each([&](int c, int e) {
       // features that are not there have dy = 0; xh only has to be finite
       const bool mine = c < NC ? at.has(c) : at.has_tail();
-      xh(c, e) = mine ? (xh(c, e) - mean) * rstd : 0.0f;
+      xh(c, e) = mine ? (xh(c, e) - r_mean) * r_rstd : 0.0f;
       dg(c, e) += g(c, e) * xh(c, e);
       db(c, e) += g(c, e);
       g(c, e) *= gm(c, e);
@@ -261,7 +272,7 @@ __global__ __launch_bounds__(WPR == 1 ? kBwdWaves * 64 : WPR * 64, WPR == 1 && N
     Row<NC> res;
     res.fill(0.0f);
     if (p.dS) res.set(rs);
-    Row<NC>::each([&](int c, int e) { res(c, e) += rstd * (g(c, e) - s1 - xh(c, e) * s2); });
+    Row<NC>::each([&](int c, int e) { res(c, e) += r_rstd * (g(c, e) - s1 - xh(c, e) * s2); });
     res.store(static_cast<TX*>(p.dX) + row * p.d, at);
   }
   if (!p.part) return;
@@ -331,7 +342,7 @@ int64_t fwd_grid(int64_t M, int wpr) {
 // many rows in flight, took 38 against 30 us for 12288 rows of 768).  Wider
 // ones: fewer, so that the partial sums stay a small part of the traffic.
 int64_t bwd_grid(int64_t M, int64_t d) {
-  const int64_t rows_per_wg = d <= 1024 ? kBwdWaves : 1, cap = d <= 1024 ? 1024 : d <= 2048 ? 512 : 256;
+  const int64_t rows_per_wg = d <= 1024 ? kBwdWaves : 1, cap = d <= 1024 ? 1024 : 256;
   const int64_t wgs = (M + rows_per_wg - 1) / rows_per_wg;
   const int64_t rounds = (wgs + cap - 1) / cap;
   return rounds ? (wgs + rounds - 1) / rounds : 0;
