@@ -38,8 +38,14 @@ constexpr int kFullTiles = 32;   // steps that repay a workgroup's start and joi
 constexpr int kMaxSplit = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 
-typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
+typedef float f32x8_u __attribute__((ext_vector_type(8), aligned(4)));
 typedef __bf16 bf16x8_u __attribute__((ext_vector_type(8), aligned(2)));
+
+// Eight values at the alignment of one.
+__device__ inline f32x8_u load8(const float* p) { return *reinterpret_cast<const f32x8_u*>(p); }
+__device__ inline f32x8_u load8(const __bf16* p) {
+  return __builtin_convertvector(*reinterpret_cast<const bf16x8_u*>(p), f32x8_u);
+}
 
 struct AttnParams {
   const void* Q;
@@ -55,15 +61,16 @@ struct AttnParams {
   float scale;
 };
 
-// The tiles of a sequence that split s of nsplit takes.
+// The tiles of a sequence that part s of at most nsplit takes; 32 bits hold
+// every count (a length is an int32).
 struct TileRange {
-  int64_t begin, end;
+  int begin, end;
 };
-__device__ inline TileRange split_tiles(int64_t len, int nsplit, int min_tiles, int s, int* used) {
-  const int64_t tiles = (len + kKeys - 1) / kKeys;
-  const int64_t per = max((tiles + nsplit - 1) / nsplit, int64_t(min_tiles));
+__device__ inline TileRange split_tiles(int len, int nsplit, int min_tiles, int s, int* used) {
+  const uint32_t tiles = (uint32_t(len) + kKeys - 1) / kKeys;
+  const uint32_t per = max((tiles + nsplit - 1) / uint32_t(nsplit), uint32_t(min_tiles));
   *used = int((tiles + per - 1) / per);
-  return {min(s * per, tiles), min((s + 1) * per, tiles)};
+  return {int(min(s * per, tiles)), int(min((s + 1) * per, tiles))};
 }
 
 // x = hi + mid + lo exactly to 24 bits, each a bf16.
@@ -82,7 +89,7 @@ __device__ inline f32x4_t mfma(bf16x8_t a, bf16x8_t b, f32x4_t c) {
 // DC: 32-wide feature chunks (D <= 32 DC).  NQ: bf16 terms of a query; NP: of
 // a probability.
 template <int DC, typename TQ, int NP>
-__global__ __launch_bounds__(kAttnWaves * 64) void attn_decode_kernel(AttnParams p) {
+__global__ __launch_bounds__(kAttnWaves * 64, DC <= 4 ? 2 : 1) void attn_decode_kernel(AttnParams p) {
   constexpr int NQ = sizeof(TQ) == 4 ? 3 : 1;
   constexpr int DT = 2 * DC;             // 16-wide feature tiles of the output
   constexpr int kRow = 16 * DT + 4;      // floats of one head's row in LDS
@@ -103,7 +110,7 @@ __global__ __launch_bounds__(kAttnWaves * 64) void attn_decode_kernel(AttnParams
   const int heads = min(16, p.G - 16 * ht);              // query heads of this workgroup
   const int head0 = hkv * p.G + 16 * ht;
 
-  int64_t len = p.lens[b];
+  int len = p.lens[b];
   bool bad = len < 0 || len > (p.max_pages << p.page_shift);
   if (bad) len = 0;
   int used;
@@ -112,21 +119,24 @@ __global__ __launch_bounds__(kAttnWaves * 64) void attn_decode_kernel(AttnParams
 
   // queries: lane n holds features 32 c + 8 g .. + 7 of head n
   bf16x8_t q[NQ][DC];
+  {
+    f32x8_u raw[DC];
 #pragma unroll
-  for (int c = 0; c < DC; ++c) {
-    float x[8];
-    const int f = 32 * c + 8 * g;
-    const bool ok = n < heads && f < p.D;
-    const TQ* src = static_cast<const TQ*>(p.Q) + b * p.ldq + int64_t(head0 + n) * p.D + f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = ok ? float(src[e]) : 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      __bf16 t[3];
-      split3(x[e], t);
-#pragma unroll
-      for (int k = 0; k < NQ; ++k) q[k][c][e] = t[k];
+    for (int c = 0; c < DC; ++c) {
+      const int f = 32 * c + 8 * g;
+      raw[c] = f32x8_u{0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+      if (n < heads && f < p.D)
+        raw[c] = load8(static_cast<const TQ*>(p.Q) + b * p.ldq + int64_t(head0 + n) * p.D + f);
     }
+#pragma unroll
+    for (int c = 0; c < DC; ++c)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        __bf16 t[3];
+        split3(raw[c][e], t);
+#pragma unroll
+        for (int k = 0; k < NQ; ++k) q[k][c][e] = t[k];
+      }
   }
 
   f32x4_t acc[DT];
@@ -134,46 +144,60 @@ __global__ __launch_bounds__(kAttnWaves * 64) void attn_decode_kernel(AttnParams
   for (int d = 0; d < DT; ++d) acc[d] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   float m = -INFINITY, l = 0.0f;
   const float c2 = p.scale * kLog2e;
-  const int64_t last = len - 1;
+  const int last = len - 1;
   const int64_t page_elems = int64_t(p.D) << p.page_shift;   // of one head's page
-  const int64_t page_mask = (int64_t(1) << p.page_shift) - 1;
+  const int page_mask = (1 << p.page_shift) - 1;
   const int32_t* row = p.table + b * p.max_pages;
 
   // Positions behind the end read the last one's place: their scores are masked
-  // and their values zeroed below.  The page ids of a step are read while the
-  // step before it computes: read on demand they put a second latency in front
-  // of every step's loads.
-  int kid = 0, vid = 0;
-  auto read_ids = [&](int64_t tile) {
-    kid = row[min(tile * kKeys + 8 * (n >> 2), last) >> p.page_shift];
-    vid = row[min(tile * kKeys + 8 * g, last) >> p.page_shift];
+  // and their values zeroed below.
+  struct Ids {
+    int k, v;
   };
-  if (r.begin + wave < r.end) read_ids(r.begin + wave);
-  for (int64_t tile = r.begin + wave; tile < r.end; tile += kAttnWaves) {
-    const int64_t kkey = tile * kKeys + 8 * (n >> 2);           // the key fragments' group of 8
-    const int64_t vkey = min(tile * kKeys + 8 * g, last & ~int64_t(7));
-    int64_t kpage = kid, vpage = vid;
-    const bool wrong = kpage < 0 || kpage >= p.n_pages || vpage < 0 || vpage >= p.n_pages;
-    if (wrong) kpage = vpage = 0;
+  auto read_ids = [&](int tile) {
+    return Ids{row[min(tile * kKeys + 8 * (n >> 2), last) >> p.page_shift],
+               row[min(tile * kKeys + 8 * g, last) >> p.page_shift]};
+  };
+  auto page_of = [&](int id) -> int64_t {
+    const bool wrong = id < 0 || id >= p.n_pages;
     bad |= wrong;
-    const __bf16* kbase = p.K + (kpage * p.Hkv + hkv) * page_elems;
-    const __bf16* vbase = p.V + (vpage * p.Hkv + hkv) * page_elems + (vkey & page_mask);
-    u32x4_t kf[2][DC], vf[DT];
+    return wrong ? 0 : id;
+  };
+  u32x4_t kf[2][DC], vf[DT];
+  auto load_k = [&](int tile, int id) {
+    const int key = tile * kKeys + 8 * (n >> 2);           // the key fragments' group of 8
+    const __bf16* base = p.K + (page_of(id) * p.Hkv + hkv) * page_elems;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const __bf16* src = kbase + (min(kkey + 4 * t + (n & 3), last) & page_mask) * p.D;
+      const __bf16* src = base + (min(key + 4 * t + (n & 3), last) & page_mask) * p.D;
 #pragma unroll
       for (int c = 0; c < DC; ++c) {
         const int f = 32 * c + 8 * g;
         kf[t][c] = *reinterpret_cast<const u32x4_t*>(src + (f < p.D ? f : 0));
       }
     }
+  };
+  auto load_v = [&](int tile, int id) {
+    const int key = min(tile * kKeys + 8 * g, last & ~7);
+    const __bf16* base = p.V + (page_of(id) * p.Hkv + hkv) * page_elems + (key & page_mask);
 #pragma unroll
-    for (int d = 0; d < DT; ++d) {
-      const int f = min(16 * d + n, p.D - 1);
-      vf[d] = *reinterpret_cast<const u32x4_t*>(vbase + (int64_t(f) << p.page_shift));
-    }
-    if (tile + kAttnWaves < r.end) read_ids(tile + kAttnWaves);
+    for (int d = 0; d < DT; ++d)
+      vf[d] = *reinterpret_cast<const u32x4_t*>(base + (int64_t(min(16 * d + n, p.D - 1)) << p.page_shift));
+  };
+
+  // The next step's keys are loaded as soon as this one's scores are formed, its
+  // values as soon as this one's are used, and the page ids a step before that,
+  // so that a wave always has loads in flight without a second set of registers.
+  int tile = r.begin + wave;
+  Ids ids = {0, 0};
+  if (tile < r.end) {
+    const Ids first = read_ids(tile);
+    if (tile + kAttnWaves < r.end) ids = read_ids(tile + kAttnWaves);
+    load_k(tile, first.k);
+    load_v(tile, first.v);
+  }
+  for (; tile < r.end; tile += kAttnWaves) {
+    const int next = tile + kAttnWaves;
     // features behind D: zero (a zero query alone would turn an infinite key into a NaN)
 #pragma unroll
     for (int c = DC - 1; c < DC; ++c)
@@ -196,7 +220,12 @@ __global__ __launch_bounds__(kAttnWaves * 64) void attn_decode_kernel(AttnParams
         for (int i = 0; i < 4; ++i) s[t][i] = __builtin_isfinite(s[t][i]) ? s[t][i] + lo[i] : s[t][i];
       }
     }
-    const int64_t left = len - (tile * kKeys + 8 * g);          // positions of this lane's 8 that count
+    const Ids now = ids;
+    if (next < r.end) {
+      if (next + kAttnWaves < r.end) ids = read_ids(next + kAttnWaves);
+      load_k(next, now.k);
+    }
+    const int left = len - (tile * kKeys + 8 * g);          // positions of this lane's 8 that count
     float mx = -INFINITY;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -232,12 +261,16 @@ __global__ __launch_bounds__(kAttnWaves * 64) void attn_decode_kernel(AttnParams
         for (int j = 0; j < 4; ++j)
           vf[d][j] &= (2 * j < left ? 0xffffu : 0u) | (2 * j + 1 < left ? 0xffff0000u : 0u);
     }
+    if (__any(alpha != 1.0f)) {   // the maximum moves in few steps but the first
+#pragma unroll
+      for (int d = 0; d < DT; ++d) acc[d] *= alpha;
+    }
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
-      acc[d] *= alpha;
 #pragma unroll
       for (int k = NP - 1; k >= 0; --k) acc[d] = mfma(as_frag(vf[d]), pf[k], acc[d]);
     }
+    if (next < r.end) load_v(next, now.v);
   }
 
   // join the waves: lane (n, g) holds features 16 d + 4 g .. + 3 of head n
@@ -292,7 +325,7 @@ __global__ __launch_bounds__(kMaxSplit) void attn_join_kernel(AttnParams p, int 
   const int b = int(blockIdx.x / uint32_t(p.H));
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int32_t length = p.lens[b];
-  int64_t len = length;
+  int len = length;
   if (len < 0 || len > (p.max_pages << p.page_shift)) len = 0;   // split 0 wrote a NaN
   int used;
   split_tiles(len, p.nsplit, p.min_tiles, 0, &used);
@@ -360,21 +393,22 @@ __global__ __launch_bounds__(256) void kv_append_kernel(AppendParams p) {
     const int64_t th = i / chunks;
     const int h = int(th % p.Hkv);
     const int64_t t = th / p.Hkv;
+    // the token's values do not wait for its place
+    const f32x8_u k = load8(static_cast<const T*>(p.K) + t * p.ldk + int64_t(h) * p.D + 8 * c);
+    const f32x8_u v = load8(static_cast<const T*>(p.V) + t * p.ldv + int64_t(h) * p.D + 8 * c);
     const int64_t s = p.seq ? p.seq[t] : t, pos = p.pos[t];
     if (s < 0 || s >= p.n_seqs || pos < 0 || (pos >> p.page_shift) >= p.max_pages) continue;
     const int64_t page = p.table[s * p.max_pages + (pos >> p.page_shift)];
     if (page < 0 || page >= p.n_pages) continue;
     const int64_t slot = pos & ((int64_t(1) << p.page_shift) - 1);
     const int64_t head = (page * p.Hkv + h) * (int64_t(p.D) << p.page_shift);
-    const T* k = static_cast<const T*>(p.K) + t * p.ldk + int64_t(h) * p.D + 8 * c;
-    const T* v = static_cast<const T*>(p.V) + t * p.ldv + int64_t(h) * p.D + 8 * c;
     bf16x8_t kk;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) kk[e] = (__bf16)float(k[e]);
+    for (int e = 0; e < 8; ++e) kk[e] = (__bf16)k[e];
     *reinterpret_cast<bf16x8_t*>(p.Kp + head + slot * p.D + 8 * c) = kk;
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      p.Vp[head + (int64_t(8 * c + e) << p.page_shift) + slot] = (__bf16)float(v[e]);
+      p.Vp[head + (int64_t(8 * c + e) << p.page_shift) + slot] = (__bf16)v[e];
   }
 }
 
