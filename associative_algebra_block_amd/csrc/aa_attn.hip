@@ -5,9 +5,8 @@
 //
 // The cache is bf16: pages of `page` positions (a power of two), keys as
 // [page id][kv head][position][feature], values as [page id][kv head][feature]
-// [position].  With the values transposed, both products read their cache
-// operand straight into matrix fragments, 16 bytes a lane, and nothing of the
-// cache passes through LDS:
+// [position].  With the values transposed, both products find 16 bytes of a
+// fragment together:
 //   S^T (keys x heads)  = K (16 keys x 32 features) . Q^T
 //   O^T (features x heads) += V^T (16 features x 32 keys) . P^T
 // The key order inside a product is free, so the 32 keys of a step are dealt
@@ -73,6 +72,45 @@ __device__ inline TileRange split_tiles(int len, int nsplit, int min_tiles, int 
   return {int(min(s * per, tiles)), int(min((s + 1) * per, tiles))};
 }
 
+// 16 bytes from each lane's own address to dst + 16 lane (dst is the same for
+// the whole wave); NT: past the caches.
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+template <bool NT>
+__device__ inline void dma16(const __bf16* src, unsigned char* dst) {
+  __builtin_amdgcn_global_load_lds(src, (lds_ptr_t)dst, 16, 0, NT ? 2 : 0);
+}
+// Until all but the last N memory operations of the wave have landed.
+template <int N>
+__device__ inline void wait_vm() {
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt((N & 15) | 0x0f70 | (N >> 4) << 14);
+  __builtin_amdgcn_sched_barrier(0);
+}
+// v[i] = 16 bytes of LDS at byte address at[i].  As one block with its wait: a
+// plain LDS read behind loads into LDS makes the compiler wait for all of them,
+// the next step's too.
+__device__ inline void read_lds4(const uint32_t* at, u32x4_t* v) {
+  asm volatile(
+      "ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_b128 %2, %6\n\tds_read_b128 %3, %7\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+      : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3])
+      : "memory");
+}
+__device__ inline void read_lds2(const uint32_t* at, u32x4_t* v) {
+  asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %3\n\ts_waitcnt lgkmcnt(0)"
+               : "=&v"(v[0]), "=&v"(v[1])
+               : "v"(at[0]), "v"(at[1])
+               : "memory");
+}
+__device__ inline uint32_t lds_address(const void* p) {
+  return uint32_t(reinterpret_cast<uintptr_t>((const __attribute__((address_space(3))) void*)p));
+}
+
+template <bool B> struct Bool {
+  static constexpr bool value = B;
+};
+
 // x = hi + mid + lo exactly to 24 bits, each a bf16.
 __device__ inline void split3(float x, __bf16* t) {
   t[0] = (__bf16)x;
@@ -93,10 +131,12 @@ __global__ __launch_bounds__(kAttnWaves * 64, DC <= 4 ? 2 : 1) void attn_decode_
   constexpr int NQ = sizeof(TQ) == 4 ? 3 : 1;
   constexpr int DT = 2 * DC;             // 16-wide feature tiles of the output
   constexpr int kRow = 16 * DT + 4;      // floats of one head's row in LDS
-  __shared__ float s_acc[kAttnWaves][16][kRow];
+  constexpr int kStage = 2048 * DT;      // a wave's keys and values of one step, and in the end its sums
+  __shared__ __align__(16) unsigned char s_stage[kAttnWaves * (kStage > 64 * kRow ? kStage : 64 * kRow)];
   __shared__ float s_ml[kAttnWaves][16][2];
+  float(*s_acc)[16][kRow] = reinterpret_cast<float(*)[16][kRow]>(s_stage);
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, g = lane >> 4;
   // parts outermost: consecutive workgroups go to different dies, and the parts
   // that only long sequences have spread over all of them (with the parts
@@ -145,85 +185,131 @@ __global__ __launch_bounds__(kAttnWaves * 64, DC <= 4 ? 2 : 1) void attn_decode_
   float m = -INFINITY, l = 0.0f;
   const float c2 = p.scale * kLog2e;
   const int last = len - 1;
-  const int64_t page_elems = int64_t(p.D) << p.page_shift;   // of one head's page
   const int page_mask = (1 << p.page_shift) - 1;
+  const int64_t page_elems = int64_t(p.D) << p.page_shift;   // of one head's page
   const int32_t* row = p.table + b * p.max_pages;
 
-  // Positions behind the end read the last one's place: their scores are masked
-  // and their values zeroed below.
-  struct Ids {
-    int k, v;
+  // A step's 32 positions are two halves of 16, which lie in one page or in two.
+  // A missing second half reads the first one's place: what lies behind the end
+  // of a sequence is read as it comes, its scores masked and its values zeroed.
+  // The ids are read by lanes 0 and 32: a scalar load would hold up the LDS
+  // operations behind it.
+  auto read_ids = [&](int tile) { return row[min(tile * kKeys + 16 * (lane >> 5), last) >> p.page_shift]; };
+  struct Halves {
+    int64_t first, second;   // element offsets of the pages
   };
-  auto read_ids = [&](int tile) {
-    return Ids{row[min(tile * kKeys + 8 * (n >> 2), last) >> p.page_shift],
-               row[min(tile * kKeys + 8 * g, last) >> p.page_shift]};
-  };
-  auto page_of = [&](int id) -> int64_t {
-    const bool wrong = id < 0 || id >= p.n_pages;
+  auto halves_of = [&](int ids) {
+    const int id0 = __builtin_amdgcn_readlane(ids, 0), id1 = __builtin_amdgcn_readlane(ids, 32);
+    const bool wrong = id0 < 0 || id0 >= p.n_pages || id1 < 0 || id1 >= p.n_pages;
     bad |= wrong;
-    return wrong ? 0 : id;
-  };
-  u32x4_t kf[2][DC], vf[DT];
-  auto load_k = [&](int tile, int id) {
-    const int key = tile * kKeys + 8 * (n >> 2);           // the key fragments' group of 8
-    const __bf16* base = p.K + (page_of(id) * p.Hkv + hkv) * page_elems;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const __bf16* src = base + (min(key + 4 * t + (n & 3), last) & page_mask) * p.D;
-#pragma unroll
-      for (int c = 0; c < DC; ++c) {
-        const int f = 32 * c + 8 * g;
-        kf[t][c] = *reinterpret_cast<const u32x4_t*>(src + (f < p.D ? f : 0));
-      }
-    }
-  };
-  auto load_v = [&](int tile, int id) {
-    const int key = min(tile * kKeys + 8 * g, last & ~7);
-    const __bf16* base = p.V + (page_of(id) * p.Hkv + hkv) * page_elems + (key & page_mask);
-#pragma unroll
-    for (int d = 0; d < DT; ++d)
-      vf[d] = *reinterpret_cast<const u32x4_t*>(base + (int64_t(min(16 * d + n, p.D - 1)) << p.page_shift));
+    Halves h;
+    h.first = (int64_t(wrong ? 0 : id0) * p.Hkv + hkv) * page_elems;
+    h.second = (int64_t(wrong ? 0 : id1) * p.Hkv + hkv) * page_elems;
+    return h;
   };
 
-  // The next step's keys are loaded as soon as this one's scores are formed, its
-  // values as soon as this one's are used, and the page ids a step before that,
-  // so that a wave always has loads in flight without a second set of registers.
-  int tile = r.begin + wave;
-  Ids ids = {0, 0};
-  if (tile < r.end) {
-    const Ids first = read_ids(tile);
-    if (tile + kAttnWaves < r.end) ids = read_ids(tile + kAttnWaves);
-    load_k(tile, first.k);
-    load_v(tile, first.v);
+  // Memory straight to the wave's own LDS, 1 KiB in a row for each load: slot
+  // 64 i + lane of load i takes one piece of 16 bytes (slots behind the last
+  // piece take that one again).  The keys' whole lines are fetched past the
+  // caches (nontemporal): they are used once.  So are the values' from pages of
+  // up to 32 positions; from larger ones a feature's 64 bytes are half a line,
+  // whose other half a neighbour wave wants.
+  const int R = p.D / 8;              // pieces of a key
+  const bool small = p.page_shift == 4;
+  unsigned char* kmine = s_stage + wave * kStage;
+  unsigned char* vmine = kmine + 1024 * DT;
+  // Slot (key, x) of the keys holds piece x - r modulo R, where r is the key's
+  // row in its fragment: the 16 rows of a fragment then lie in different banks.
+  const uint32_t by_row = (65536u + R - 1) / uint32_t(R);   // y / R = y * by_row >> 16 for all y < 33 R
+  int koff[DT];                       // offset of this lane's piece of load i, from the page of its half
+#pragma unroll
+  for (int i = 0; i < DT; ++i) {
+    const int slot = min(64 * i + lane, 32 * R - 1);
+    const int key = int(uint32_t(slot) * by_row >> 16);
+    const int y = slot - key * R + 32 * R - (((key >> 3) << 2) | (key & 3));
+    koff[i] = key * p.D + 8 * (y - int(uint32_t(y) * by_row >> 16) * R);
   }
-  for (; tile < r.end; tile += kAttnWaves) {
-    const int next = tile + kAttnWaves;
-    // features behind D: zero (a zero query alone would turn an infinite key into a NaN)
+  auto load_k = [&](int tile, const Halves& h) {
+    const __bf16* k0 = p.K + h.first + int64_t((tile * kKeys) & page_mask) * p.D;
+    const __bf16* k1 = p.K + h.second + int64_t((tile * kKeys + 16) & page_mask) * p.D - 16 * p.D;
 #pragma unroll
-    for (int c = DC - 1; c < DC; ++c)
-      if (32 * c + 8 * g >= p.D) kf[0][c] = kf[1][c] = u32x4_t{0u, 0u, 0u, 0u};
+    for (int i = 0; i < DT; ++i) dma16<true>((koff[i] < 16 * p.D ? k0 : k1) + koff[i], kmine + 1024 * i);
+  };
+  // Values: [half][feature][16] from pages of 16, else [feature][32], the pieces
+  // of a feature turned by its row in the fragment for the banks' sake.
+  auto load_wide = [&](auto nt, int tile, const Halves& h) {
+    const __bf16* v0 = p.V + h.first + ((tile * kKeys) & page_mask);
+#pragma unroll
+    for (int i = 0; i < DT; ++i) {
+      const int slot = min(64 * i + lane, 4 * p.D - 1);
+      dma16<nt.value>(v0 + (int64_t(slot >> 2) << p.page_shift) + ((slot - (slot >> 4)) & 3) * 8, vmine + 1024 * i);
+    }
+  };
+  auto load_v = [&](int tile, const Halves& h) {
+    if (small) {
+      const __bf16* v0 = p.V + h.first;
+      const __bf16* v1 = p.V + h.second - 16 * p.D;
+#pragma unroll
+      for (int i = 0; i < DT; ++i) {
+        const int slot = min(64 * i + lane, 4 * p.D - 1);
+        const int half = slot < 2 * p.D ? 0 : 1, d = (slot - half * 2 * p.D) >> 1;
+        dma16<true>((half ? v1 : v0) + (slot ^ ((d >> 3) & 1)) * 8, vmine + 1024 * i);
+      }
+    } else if (p.page_shift == 5) {
+      load_wide(Bool<true>(), tile, h);
+    } else {
+      load_wide(Bool<false>(), tile, h);
+    }
+  };
+  uint32_t kslot[2 * DC];             // LDS address of this lane's piece of chunk c in fragment t: row n there is
+#pragma unroll
+  for (int c = 0; c < DC; ++c) {      // key 8 (n / 4) + 4 t + n mod 4
+    const int piece = min(4 * c + g, R - 1), y = piece + n;
+    kslot[c] = lds_address(kmine) + ((8 * (n >> 2) + (n & 3)) * R + y - int(uint32_t(y) * by_row >> 16) * R) * 16;
+    kslot[DC + c] = kslot[c] + 64 * R;
+  }
+  const uint32_t vfrag = lds_address(vmine) + (small ? (g >> 1) * 32 * p.D + n * 32 + ((g ^ (n >> 3)) & 1) * 16
+                                                     : n * 64 + ((g + (n >> 2)) & 3) * 16);
+  const int vstep = small ? 512 : 1024;   // bytes from 16 features to the next
 
-    f32x4_t s[2];
+  // The next step's keys are on their way as soon as this one's have left LDS,
+  // its values likewise, and the page ids a step before that.  Every step issues
+  // the ids, DT loads of keys and DT of values in this order, so a count says
+  // which have landed.
+  int tile = r.begin + wave;
+  int ids = 0;
+  auto step = [&](auto more) {
+    const int next = tile + kAttnWaves;
+    wait_vm<DT>();                    // keys (behind them: this step's values)
+    f32x4_t s[2], lo[2];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      s[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int t = 0; t < 2; ++t) s[t] = lo[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int c = 0; c < DC; ++c) s[t] = mfma(as_frag(kf[t][c]), q[0][c], s[t]);
-      if constexpr (NQ > 1) {
-        f32x4_t lo = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < 2 * DC; j += 2) {   // pieces j and j + 1 of [fragment][chunk]
+      u32x4_t kf[2];
+      read_lds2(kslot + j, kf);
 #pragma unroll
-        for (int k = NQ - 1; k >= 1; --k)     // the smallest terms first
+      for (int x = 0; x < 2; ++x) {
+        const int t = (j + x) / DC, c = (j + x) % DC;
+        // features behind D: zero (a zero query alone would turn an infinite key into a NaN)
+        if (c == DC - 1 && 4 * c + g >= R) kf[x] = u32x4_t{0u, 0u, 0u, 0u};
+        s[t] = mfma(as_frag(kf[x]), q[0][c], s[t]);
 #pragma unroll
-          for (int c = 0; c < DC; ++c) lo = mfma(as_frag(kf[t][c]), q[k][c], lo);
-        // an infinite key: the leading term has the query's sign, the others need not
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[t][i] = __builtin_isfinite(s[t][i]) ? s[t][i] + lo[i] : s[t][i];
+        for (int i = NQ - 1; i >= 1; --i) lo[t] = mfma(as_frag(kf[x]), q[i][c], lo[t]);
       }
     }
-    const Ids now = ids;
-    if (next < r.end) {
-      if (next + kAttnWaves < r.end) ids = read_ids(next + kAttnWaves);
-      load_k(next, now.k);
+    if constexpr (NQ > 1) {
+      // an infinite key: the leading term has the query's sign, the others need not
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[t][i] = __builtin_isfinite(s[t][i]) ? s[t][i] + lo[t][i] : s[t][i];
+    }
+    Halves now = {0, 0};
+    if constexpr (more.value) {
+      now = halves_of(ids);
+      ids = read_ids(min(next + kAttnWaves, r.end - 1));
+      load_k(next, now);
     }
     const int left = len - (tile * kKeys + 8 * g);          // positions of this lane's 8 that count
     float mx = -INFINITY;
@@ -254,23 +340,43 @@ __global__ __launch_bounds__(kAttnWaves * 64, DC <= 4 ? 2 : 1) void attn_decode_
         for (int k = 0; k < NP; ++k) pf[k][4 * t + i] = term[k];
       }
     l = l * alpha + sum;
-    if (left < 8) {   // what lies behind the end may be anything, NaN included: 0 . NaN is no zero
+    // what lies behind the end may be anything, NaN included, and 0 . NaN is no zero
+    uint32_t keep[4];
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          vf[d][j] &= (2 * j < left ? 0xffffu : 0u) | (2 * j + 1 < left ? 0xffff0000u : 0u);
-    }
+    for (int j = 0; j < 4; ++j) keep[j] = (2 * j < left ? 0xffffu : 0u) | (2 * j + 1 < left ? 0xffff0000u : 0u);
+    const bool tail = tile * kKeys + kKeys > len;
+    wait_vm<more.value ? DT + 1 : 0>();   // values (behind them: ids and the next keys)
     if (__any(alpha != 1.0f)) {   // the maximum moves in few steps but the first
 #pragma unroll
       for (int d = 0; d < DT; ++d) acc[d] *= alpha;
     }
 #pragma unroll
-    for (int d = 0; d < DT; ++d) {
+    for (int d = 0; d < DT; d += 2) {
+      const uint32_t at[2] = {vfrag + d * vstep, vfrag + (d + 1) * vstep};
+      u32x4_t v[2];
+      read_lds2(at, v);       // rows behind D hold anything and are not stored
 #pragma unroll
-      for (int k = NP - 1; k >= 0; --k) acc[d] = mfma(as_frag(vf[d]), pf[k], acc[d]);
+      for (int x = 0; x < 2; ++x) {
+        if (tail) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[x][j] &= keep[j];
+        }
+#pragma unroll
+        for (int k = NP - 1; k >= 0; --k) acc[d + x] = mfma(as_frag(v[x]), pf[k], acc[d + x]);
+      }
     }
-    if (next < r.end) load_v(next, now.v);
+    if constexpr (more.value) {
+      load_v(next, now);
+    }
+  };
+  if (tile < r.end) {
+    const int first_ids = read_ids(tile);
+    ids = read_ids(min(tile + kAttnWaves, r.end - 1));
+    const Halves first = halves_of(first_ids);
+    load_k(tile, first);
+    load_v(tile, first);
+    for (; tile + kAttnWaves < r.end; tile += kAttnWaves) step(Bool<true>());
+    step(Bool<false>());
   }
 
   // join the waves: lane (n, g) holds features 16 d + 4 g .. + 3 of head n
@@ -281,6 +387,7 @@ __global__ __launch_bounds__(kAttnWaves * 64, DC <= 4 ? 2 : 1) void attn_decode_
     s_ml[wave][n][0] = m;
     s_ml[wave][n][1] = l;
   }
+  __syncthreads();   // the sums of one wave overlie what another may still read
 #pragma unroll
   for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4_t*>(&s_acc[wave][n][16 * d + 4 * g]) = acc[d];
   __syncthreads();
