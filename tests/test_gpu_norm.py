@@ -74,7 +74,8 @@ def reference(x, gamma, beta, eps):
 # widths at each split's edges (256, 512, 768, 1024, 2048, 4096, 8192, 16384), odd ones among them
 SIZES = [(1, 1), (3, 2), (1, 3), (5, 7), (2, 64), (9, 255), (4, 256), (7, 257), (3, 511), (6, 513), (1, 768), (37, 768),
          (5, 769), (11, 1024), (10, 1025), (3, 2047), (8, 2048), (5, 2049), (2, 4096), (3, 4097), (2, 8192), (3, 8193),
-         (1, 16383), (2, 16384), (4200, 768), (2111, 100), (600, 4100)]
+         (1, 16383), (2, 16384), (4200, 768), (2111, 100), (600, 4100),
+         (9000, 1030)]   # outputs of more than 32 MB, which go past the caches
 
 
 @pytest.mark.parametrize("M,d", SIZES)
