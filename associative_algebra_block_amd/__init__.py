@@ -335,46 +335,17 @@ def aa_project_bwd_weight(plan: Plan, X, dY, dW_packed, M=None, pos_offset=0, ro
         _stream(stream)), "aa_project_bwd_weight")
 
 
-# The operators below take tensors only: their sizes and types come from them.
-# Their checks are most of what a call of a few microseconds costs on the host,
-# so each tensor passes one line of tests and the reason is looked for only
-# where that fails; the stream comes from the function behind
-# torch.cuda.current_stream (2.5 against 0.1 us).
+# ------------------------------------- the operators around the row-typed FFN ---
+#
+# They take torch tensors, on the current device, and go by their shapes, types
+# and strides.  The extension module _aa_binding (csrc/aa_binding.cpp) checks
+# them and calls the entry points: a TypeError or ValueError names a tensor that
+# does not fit, an AAError is a call that the library refused.
 
-def _tensor(t, name, shape, dtypes, device):
-    """Device pointer of a dense tensor of the given shape and one of the
-    given dtypes on the GPU of index `device` (None passed through)."""
-    if t is None:
-        return None
-    if isinstance(t, torch.Tensor):
-        if t.shape == shape and t.dtype in dtypes and t.get_device() == device and t.is_contiguous():
-            return t.data_ptr()
-        if t.dtype not in dtypes:
-            raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-        if t.shape != shape:
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if t.get_device() != device:
-            raise ValueError(f"{name}: on {t.device}, expected cuda:{device}")
-        raise ValueError(f"{name}: must be contiguous")
-    raise TypeError(f"{name}: expected a tensor")
+_MARSHAL = None
 
 
-def _call_device(t, name):
-    """The GPU index of a call's first operand, which must be the current
-    device: the launch goes to a stream of the current device."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a tensor")
-    index = t.get_device()
-    if index < 0:
-        raise ValueError(f"{name}: must be a device tensor")
-    if index != torch._C._cuda_getDevice():
-        raise ValueError(f"{name}: on {t.device}, but the current device is {torch._C._cuda_getDevice()}")
-    return index
-
-
-def _stream_on(stream, device):
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device)
+def _given_stream(stream, device):
     if isinstance(stream, torch.cuda.Stream):
         if stream.device.index != device:
             raise ValueError(f"stream: on {stream.device}, expected cuda:{device}")
@@ -382,37 +353,30 @@ def _stream_on(stream, device):
     return int(stream)
 
 
-def _workspace(workspace, device):
-    """(pointer, bytes) of a workspace tensor or None."""
-    if workspace is None:
-        return None, 0
-    if not isinstance(workspace, torch.Tensor):
-        raise TypeError("workspace: expected a tensor")
-    if workspace.get_device() != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace: must be contiguous and on cuda:{device}")
-    return workspace.data_ptr(), workspace.nbytes
-
-
-_FLOATS = (torch.bfloat16, torch.float32)
-_F32 = (torch.float32,)
+def _marshal():
+    """The extension module, bound to the loaded library (once)."""
+    global _MARSHAL
+    if _MARSHAL is None:
+        lib = load()
+        try:
+            from . import _aa_binding
+        except ImportError as e:
+            raise RuntimeError("the Python binding _aa_binding.so is not built: run "
+                               "`python -m associative_algebra_block_amd.build`") from e
+        address = [ctypes.cast(getattr(lib, n), _c_p).value for n in
+                   ("aa_layernorm_fwd", "aa_layernorm_bwd", "aa_kv_append", "aa_attn_decode", "aa_moe_ffn_fwd")]
+        _aa_binding.bind(*address, torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream, _given_stream)
+        _MARSHAL = _aa_binding
+    return _MARSHAL
 
 
 def aa_layernorm_fwd(X, gamma, beta, Y, delta=None, S=None, mean=None, rstd=None, eps=1e-5, stream=None):
     """Y = layernorm(X [+ delta]) over the last dimension of the M x d tensor
     X; with delta the sum goes to S (which may be X).  gamma and beta may be
     None; mean and rstd (M float32 values each) are for the backward pass."""
-    dev = _call_device(X, "X")
-    shape = X.shape
-    if len(shape) != 2:
-        raise ValueError("X: expected two dimensions")
-    M, d = shape
-    _check(load().aa_layernorm_fwd(
-        _tensor(X, "X", shape, _FLOATS, dev), _tensor(delta, "delta", shape, _FLOATS, dev),
-        _tensor(gamma, "gamma", (d,), _F32, dev), _tensor(beta, "beta", (d,), _F32, dev),
-        _tensor(S, "S", shape, (X.dtype,), dev), _tensor(Y, "Y", shape, _FLOATS, dev),
-        _tensor(mean, "mean", (M,), _F32, dev), _tensor(rstd, "rstd", (M,), _F32, dev), M, d, eps,
-        _DTYPES[X.dtype], AA_F32 if delta is None else _DTYPES[delta.dtype], _DTYPES[Y.dtype], _stream_on(stream, dev)),
-        "aa_layernorm_fwd")
+    st = (_MARSHAL or _marshal()).layernorm_fwd(X, gamma, beta, Y, delta, S, mean, rstd, eps, stream)
+    if st:
+        _check(st, "aa_layernorm_fwd")
 
 
 def aa_layernorm_bwd_workspace(M: int, d: int) -> int:
@@ -425,73 +389,20 @@ def aa_layernorm_bwd_workspace(M: int, d: int) -> int:
 def aa_layernorm_bwd(X, dY, gamma, mean, rstd, dX, dgamma=None, dbeta=None, dS=None, workspace=None, stream=None):
     """Gradients of aa_layernorm_fwd: X is the normalised tensor (S where the
     forward call had delta), dS the residual path's gradient (may be dX)."""
-    dev = _call_device(X, "X")
-    shape = X.shape
-    if len(shape) != 2:
-        raise ValueError("X: expected two dimensions")
-    M, d = shape
-    xt = (X.dtype,)
-    ws, nbytes = _workspace(workspace, dev)
-    _check(load().aa_layernorm_bwd(
-        _tensor(X, "X", shape, _FLOATS, dev), _tensor(dY, "dY", shape, _FLOATS, dev),
-        _tensor(gamma, "gamma", (d,), _F32, dev), _tensor(mean, "mean", (M,), _F32, dev),
-        _tensor(rstd, "rstd", (M,), _F32, dev), _tensor(dS, "dS", shape, xt, dev), _tensor(dX, "dX", shape, xt, dev),
-        _tensor(dgamma, "dgamma", (d,), _F32, dev), _tensor(dbeta, "dbeta", (d,), _F32, dev), M, d,
-        _DTYPES[X.dtype], _DTYPES[dY.dtype], ws, nbytes, _stream_on(stream, dev)), "aa_layernorm_bwd")
-
-
-_I32 = (torch.int32,)
-_BF16 = (torch.bfloat16,)
-
-
-def _token_rows(t, name, n, heads, dim, dtypes, device):
-    """(pointer, row stride) of n rows of heads x dim values, [n, heads * dim]
-    or [n, heads, dim]; a row is dense, the rows may lie further apart."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if t.get_device() != device:
-        raise ValueError(f"{name}: on {t.device}, expected cuda:{device}")
-    shape, width = t.shape, heads * dim
-    if shape != (n, width) and shape != (n, heads, dim):
-        raise ValueError(f"{name}: shape {tuple(shape)}, expected {(n, width)} or {(n, heads, dim)}")
-    stride = t.stride()
-    if n and (stride[-1] != 1 and shape[-1] > 1 or len(shape) == 3 and heads > 1 and stride[1] != dim):
-        raise ValueError(f"{name}: the values of a token must be contiguous")
-    return t.data_ptr(), stride[0] if n > 1 else width
-
-
-def _cache_sizes(k_pages, v_pages, page_table):
-    """(n_pages, n_kv_heads, page_size, head_dim, n_seqs, max_pages, shapes of the two)."""
-    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages"), (page_table, "page_table")):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name}: expected a tensor")
-    kshape, tshape = k_pages.shape, page_table.shape
-    if len(kshape) != 4 or len(tshape) != 2:
-        raise ValueError("k_pages: expected four dimensions, page_table: two")
-    n_pages, hkv, page, dim = kshape
-    return n_pages, hkv, page, dim, tshape[0], tshape[1], kshape, (n_pages, hkv, dim, page), tshape
+    st = (_MARSHAL or _marshal()).layernorm_bwd(X, dY, gamma, mean, rstd, dX, dgamma, dbeta, dS, workspace, stream)
+    if st:
+        _check(st, "aa_layernorm_bwd")
 
 
 def aa_kv_append(K, V, k_pages, v_pages, page_table, pos, seq=None, stream=None):
     """Write the keys and values of n tokens ([n, kv heads * head dim] or
     [n, kv heads, head dim], rows of any stride) to their places in the cache:
-    token t to position pos[t] of sequence seq[t] (None: sequence t)."""
-    dev = _call_device(k_pages, "k_pages")
-    n_pages, hkv, page, dim, n_seqs, max_pages, kshape, vshape, tshape = _cache_sizes(k_pages, v_pages, page_table)
-    if not isinstance(pos, torch.Tensor) or pos.dim() != 1:
-        raise ValueError("pos: expected a tensor of one dimension")
-    n = len(pos)
-    k, ldk = _token_rows(K, "K", n, hkv, dim, _FLOATS, dev)
-    v, ldv = _token_rows(V, "V", n, hkv, dim, (K.dtype,), dev)
-    _check(load().aa_kv_append(
-        k, v, ldk, ldv, _DTYPES[K.dtype],
-        _tensor(k_pages, "k_pages", kshape, _BF16, dev),
-        _tensor(v_pages, "v_pages", vshape, _BF16, dev), n_pages, page, hkv, dim,
-        _tensor(page_table, "page_table", tshape, _I32, dev), n_seqs, max_pages,
-        _tensor(seq, "seq", (n,), _I32, dev), _tensor(pos, "pos", (n,), _I32, dev), n, _stream_on(stream, dev)),
-        "aa_kv_append")
+    token t to position pos[t] of sequence seq[t] (None: sequence t).  k_pages
+    is [pages, kv heads, page size, head dim], v_pages [pages, kv heads, head
+    dim, page size], page_table [sequences, pages of one] (int32)."""
+    st = (_MARSHAL or _marshal()).kv_append(K, V, k_pages, v_pages, page_table, pos, seq, stream)
+    if st:
+        _check(st, "aa_kv_append")
 
 
 def aa_attn_decode_workspace(n_seqs, n_heads, n_kv_heads, head_dim, page_size, max_pages) -> int:
@@ -503,24 +414,12 @@ def aa_attn_decode_workspace(n_seqs, n_heads, n_kv_heads, head_dim, page_size, m
 
 
 def aa_attn_decode(Q, k_pages, v_pages, page_table, lengths, O, scale, workspace=None, stream=None):
-    """O [n_seqs, heads, head dim] = attention of the queries Q ([n_seqs,
-    heads * head dim] or [n_seqs, heads, head dim], rows of any stride) over
+    """O [sequences, heads, head dim] = attention of the queries Q ([sequences,
+    heads * head dim] or [sequences, heads, head dim], rows of any stride) over
     the first lengths[s] positions of each sequence."""
-    dev = _call_device(k_pages, "k_pages")
-    n_pages, hkv, page, dim, n_seqs, max_pages, kshape, vshape, tshape = _cache_sizes(k_pages, v_pages, page_table)
-    if not isinstance(O, torch.Tensor) or O.dim() != 3:
-        raise ValueError("O: expected a tensor of three dimensions")
-    heads = O.shape[1]
-    q, ldq = _token_rows(Q, "Q", n_seqs, heads, dim, _FLOATS, dev)
-    ws, nbytes = _workspace(workspace, dev)
-    _check(load().aa_attn_decode(
-        q, ldq, _DTYPES[Q.dtype],
-        _tensor(k_pages, "k_pages", kshape, _BF16, dev),
-        _tensor(v_pages, "v_pages", vshape, _BF16, dev), n_pages, page, heads, hkv, dim,
-        _tensor(page_table, "page_table", tshape, _I32, dev), n_seqs, max_pages,
-        _tensor(lengths, "lengths", (n_seqs,), _I32, dev), scale,
-        _tensor(O, "O", (n_seqs, heads, dim), _FLOATS, dev), _DTYPES[O.dtype], ws, nbytes, _stream_on(stream, dev)),
-        "aa_attn_decode")
+    st = (_MARSHAL or _marshal()).attn_decode(Q, k_pages, v_pages, page_table, lengths, O, scale, workspace, stream)
+    if st:
+        _check(st, "aa_attn_decode")
 
 
 def aa_moe_ffn_workspace(up: Plan, down: Plan, n_experts: int, top_k: int, M: int) -> int:
@@ -536,19 +435,11 @@ def aa_moe_ffn_fwd(up: Plan, down: Plan, X, Wr, Wg_packed, Wu_packed, Wd_packed,
     """Y = the mixture-of-experts layer of X [M, D] with the router weight Wr
     [experts, D] and the experts' packed weights [experts, D * F]; experts and
     weights ([M, top_k]) receive the choice."""
-    dev = _call_device(X, "X")
-    if X.dim() != 2 or not isinstance(Wr, torch.Tensor) or Wr.dim() != 2:
-        raise ValueError("X and Wr: expected two dimensions")
-    M, E, D, nw = X.shape[0], Wr.shape[0], up.d_in, up.d_in * up.d_out
-    top_k = int(top_k)
-    ws, nbytes = _workspace(workspace, dev)
-    _check(load().aa_moe_ffn_fwd(
-        up.handle, down.handle, _tensor(X, "X", (M, D), _BF16, dev), _tensor(Wr, "Wr", (E, D), _BF16, dev), E, top_k,
-        1 if normalize else 0, _tensor(Wg_packed, "Wg_packed", (E, nw), _BF16, dev),
-        _tensor(Wu_packed, "Wu_packed", (E, nw), _BF16, dev), _tensor(Wd_packed, "Wd_packed", (E, nw), _BF16, dev),
-        _tensor(Y, "Y", (M, D), (down.out_torch_dtype,), dev), _tensor(experts, "experts", (M, top_k), _I32, dev),
-        _tensor(weights, "weights", (M, top_k), _F32, dev), M, int(pos_offset),
-        _tensor(row_types, "row_types", (M,), _I32, dev), ws, nbytes, _stream_on(stream, dev)), "aa_moe_ffn_fwd")
+    st = (_MARSHAL or _marshal()).moe_ffn_fwd(
+        up.handle, down.handle, up.d_in, up.d_out, down.out_dtype, X, Wr, Wg_packed, Wu_packed, Wd_packed, Y, top_k,
+        normalize, experts, weights, workspace, pos_offset, row_types, stream)
+    if st:
+        _check(st, "aa_moe_ffn_fwd")
 
 
 def _event(ev):

@@ -1,10 +1,12 @@
-"""Build libaa.so in-tree with hipcc for gfx950.
+"""Build libaa.so in-tree with hipcc for gfx950, and the Python binding.
 
     python -m associative_algebra_block_amd.build
 
 compiles the HIP kernels, the host plan code and the C entry points into
 associative_algebra_block_amd/libaa.so.  hipcc cross-compiles the device code,
-so no GPU is needed.  Only symbols named aa_* are exported.
+so no GPU is needed.  Only symbols named aa_* are exported.  Beside it the
+extension module _aa_binding.so (host code against torch's headers) marshals
+the arguments of the operators around the FFN.
 """
 from __future__ import annotations
 
@@ -20,6 +22,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libaa.so")
+BINDING = os.path.join(HERE, "_aa_binding.so")
 
 SOURCES = ["aa_plan.cpp", "aa_api.cpp", "aa_kernels.hip", "aa_backward.hip", "aa_small.hip", "aa_tile32.hip",
            "aa_api_ops.cpp", "aa_norm.hip", "aa_attn.hip", "aa_moe.hip"]
@@ -42,8 +45,27 @@ def hipcc() -> str:
     raise RuntimeError("hipcc not found; the HIP toolchain is required to build libaa.so")
 
 
+def binding_command(out: str) -> list:
+    """The host compiler's line for the extension module."""
+    import sysconfig
+
+    import torch
+    cxx = shutil.which("g++") or shutil.which("c++") or shutil.which("clang++")
+    if not cxx:
+        raise RuntimeError("no C++ compiler found; it is required to build the Python binding")
+    root = os.path.dirname(torch.__file__)
+    return [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(root, "include"),
+            "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+            os.path.join(CSRC, "aa_binding.cpp"), "-o", out,
+            "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10",
+            "-Wl,-rpath," + os.path.join(root, "lib")]
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every source and link libaa.so.  Returns the library path."""
+    """Compile every source, link libaa.so and build the Python binding.
+    Returns the library path."""
     cc = hipcc()
     with tempfile.TemporaryDirectory(prefix="aa_build_") as tmp:
         objs, cmds = [], []
@@ -52,6 +74,7 @@ def build(verbose: bool = False) -> str:
             lang = ["-x", "hip"] if src.endswith(".hip") else []
             cmds.append([cc, *HIP_FLAGS, *lang, "-I", INCLUDE, "-I", CSRC, "-c", os.path.join(CSRC, src), "-o", obj])
             objs.append(obj)
+        cmds.append(binding_command(BINDING + ".tmp"))
         # the translation units are independent: compile them side by side
         with ThreadPoolExecutor(max_workers=len(cmds)) as ex:
             for f in [ex.submit(_run, c, verbose) for c in cmds]:
@@ -64,6 +87,7 @@ def build(verbose: bool = False) -> str:
                f"-Wl,--version-script={vscript}", "-Wl,-rpath,/opt/rocm/lib"]
         _run(cmd, verbose)
         os.replace(out_tmp, LIB)
+        os.replace(BINDING + ".tmp", BINDING)
     return LIB
 
 

@@ -182,3 +182,14 @@ def test_binding_takes_device_tensors_only():
             f()
     with pytest.raises(TypeError):
         aa.aa_layernorm_fwd(1234, None, None, 1234)
+
+
+def test_missing_binding_fails_loudly(monkeypatch):
+    """Without the extension module the operators' calls raise: there is no
+    other path."""
+    import sys
+    monkeypatch.setattr(aa, "_MARSHAL", None)
+    monkeypatch.delattr(aa, "_aa_binding", raising=False)
+    monkeypatch.setitem(sys.modules, "associative_algebra_block_amd._aa_binding", None)
+    with pytest.raises(RuntimeError, match="is not built"):
+        aa.aa_layernorm_fwd(torch.zeros(1, 1), None, None, torch.zeros(1, 1))
