@@ -237,24 +237,23 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(MoeParams p) {
   __syncthreads();
   rank_experts<false>(s_key, s_upper, p.E, s_place);
   __syncthreads();
-  for (int e = threadIdx.x; e < p.E; e += kUpThreads) {
-    const int place = s_place[e];
-    if (place == 0) atomicAdd(&s_hits[0], 1);
-    if (place == rank) atomicAdd(&s_hits[1], 1);
-    if (place < p.top_k) atomicAdd(&s_hits[2], 1);
-  }
-  __syncthreads();
+  auto find = [&] {   // the experts at this workgroup's place and at the first
+    for (int e = threadIdx.x; e < p.E; e += kUpThreads) {
+      const int place = s_place[e];
+      if (place == 0) s_top = s_key[e], atomicAdd(&s_hits[0], 1);
+      if (place == rank) s_expert = e, atomicAdd(&s_hits[1], 1);
+      if (place < p.top_k) atomicAdd(&s_hits[2], 1);
+    }
+    __syncthreads();
+  };
+  find();
   if (s_hits[0] != 1 || s_hits[1] != 1 || s_hits[2] != p.top_k) {   // the same for all threads
     for (int e = threadIdx.x; e < p.E; e += kUpThreads) s_place[e] = 0;
     __syncthreads();
     rank_experts<true>(s_key, s_upper, p.E, s_place);
     __syncthreads();
+    find();
   }
-  for (int e = threadIdx.x; e < p.E; e += kUpThreads) {
-    if (s_place[e] == rank) s_expert = e;
-    if (s_place[e] == 0) s_top = s_key[e];
-  }
-  __syncthreads();
   const int expert = __builtin_amdgcn_readfirstlane(s_expert);
   if (blockIdx.x == 0) {   // this pair's weight, for the next kernel and the caller
     const uint64_t top_key = s_top;
