@@ -17,6 +17,8 @@
 // of as many bytes takes 27; one row takes 2.8 us, which a launch costs anyhow.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "aa_device.h"
 #include "aa_internal.h"
 
@@ -233,7 +235,8 @@ struct NormBwdParams {
 // atomics, so the result does not depend on the order of execution.
 constexpr int kBwdWaves = 4;
 template <typename TX, typename TY, int WPR, int NC>
-__global__ __launch_bounds__(WPR == 1 ? kBwdWaves * 64 : WPR * 64, WPR == 1 && NC <= 3 ? 4 : 1) void norm_bwd_kernel(NormBwdParams p) {
+__global__ __launch_bounds__(WPR == 1 ? kBwdWaves * 64 : WPR * 64, WPR == 1 && NC <= 3 ? 4 : 1)
+void norm_bwd_kernel(NormBwdParams p) {
   constexpr int kRowsPerWg = WPR == 1 ? kBwdWaves : 1;
   constexpr bool kAhead = WPR > 1 && NC <= 4;   // the next row is on its way while this one is reduced
   __shared__ float slots[2 * WPR];
@@ -364,27 +367,46 @@ int32_t past_caches(int64_t values, int64_t bytes_each) { return values * bytes_
 int64_t size_of(aa_dtype_t t) { return t == AA_F32 ? 4 : 2; }
 
 // Workgroups of the backward kernel, each of which writes 2 d partial sums.
-// Narrow rows: what fits the chip at once (1024 of 4 waves; 512 of 8 waves, as
-// many rows in flight, took 38 against 30 us for 12288 rows of 768).  Wider
-// ones: fewer, so that the partial sums stay a small part of the traffic.
-int64_t bwd_grid(int64_t M, int64_t d) {
-  const int64_t rows_per_wg = d <= 1024 ? kBwdWaves : 1, cap = d <= 1024 ? 1024 : 256;
-  const int64_t wgs = (M + rows_per_wg - 1) / rows_per_wg;
+// One wave a row: 512 (12288 float32 rows of 768 with dS take 33.6, 29.7 and
+// 31.2 us with 256, 512 and 1024).  Wider rows: at least eight a workgroup from
+// 256 on (1000 rows of 2048 take 14.1 us with 256 and 17.2 with 512, whose sums
+// take longer to write and join than the rows), and not so many that the rows in
+// flight, 4 MB, outgrow the L2s: 4600 float32 rows of 2048 take 29.4, 23.5 and
+// 24.8 us with 256, 512 and 1024; 8000 bf16 rows 49.4, 43.3 and 40.1; 10000 rows
+// of 4096 with 256 and 512: 76 and 85 in float32, 77 and 63 in bf16.
+int64_t bwd_grid(int64_t M, int64_t d, int64_t size) {
+  const bool narrow = d <= 1024;
+  const int64_t wgs = narrow ? (M + kBwdWaves - 1) / kBwdWaves : M;
+  const int64_t fit = std::min<int64_t>(std::max<int64_t>((int64_t(4) << 20) / (d * size), 256), 1024);
+  const int64_t cap = narrow ? 512 : std::min<int64_t>(fit, std::max<int64_t>(M / 8, 256));
   const int64_t rounds = (wgs + cap - 1) / cap;
   return rounds ? (wgs + rounds - 1) / rounds : 0;
 }
 
-// Calls f with the split of a row of d features: waves per row, chunks.
-#define AA_NORM_SPLIT(d, CALL)          \
-  do {                                  \
-    if ((d) <= 256) CALL(1, 1);         \
-    else if ((d) <= 512) CALL(1, 2);    \
-    else if ((d) <= 768) CALL(1, 3);    \
-    else if ((d) <= 1024) CALL(1, 4);   \
-    else if ((d) <= 2048) CALL(4, 2);   \
-    else if ((d) <= 4096) CALL(4, 4);   \
-    else if ((d) <= 8192) CALL(4, 8);   \
-    else CALL(8, 8);                    \
+// Calls CALL(waves per row, chunks) for a row of d features.  Up to 1024 one
+// wave a row, no barrier: 12288 float32 rows of 768 take 19.3 us forward and 31.7
+// backward, with four waves 21.3 and 33.3 (64 rows: 3.6 and 3.3 forward).
+// Beyond, 8 to 32 features a lane:
+//   2048 (4608 float32 rows)  4 x 8 features 19.6, 8 x 4 21.6, 1 x 32 19.1 us
+//                             forward, which one wave loses with few rows (64:
+//                             3.6, 3.5 and 4.6 us)
+//   4096 (2048 bf16 rows)     4 x 16 11.2, 8 x 8 12.6 us forward; backward, where
+//                             a lane holds three rows, the other way round (2300
+//                             float32 rows: 25.2 and 23.1)
+//   8192 (1152 float32 rows)  4 x 32 20.5, 8 x 16 20.1 us forward, 40.5 and 33.4
+//                             backward
+//   16384 (576 float32 rows)  8 x 32 23.8, 16 x 16 23.5 us forward, 55 and 123
+//                             backward (a wave of 16 has registers for half a row)
+#define AA_NORM_SPLIT(d, CALL, SPLIT4096) \
+  do {                                    \
+    if ((d) <= 256) CALL(1, 1);           \
+    else if ((d) <= 512) CALL(1, 2);      \
+    else if ((d) <= 768) CALL(1, 3);      \
+    else if ((d) <= 1024) CALL(1, 4);     \
+    else if ((d) <= 2048) CALL(4, 2);     \
+    else if ((d) <= 4096) SPLIT4096;      \
+    else if ((d) <= 8192) CALL(8, 4);     \
+    else CALL(8, 8);                      \
   } while (0)
 
 template <typename TX, typename TY>
@@ -392,17 +414,17 @@ void launch_fwd(const NormFwdParams& p, hipStream_t stream) {
 #define AA_CALL(WPR, NC)                                                                            \
   launch((norm_fwd_kernel<TX, TY, WPR, NC>), dim3(uint32_t(fwd_grid(p.M, WPR))), dim3(WPR == 1 ? 256 : WPR * 64), 0u, \
          stream, p)
-  AA_NORM_SPLIT(p.d, AA_CALL);
+  AA_NORM_SPLIT(p.d, AA_CALL, AA_CALL(4, 4));
 #undef AA_CALL
 }
 
 template <typename TX, typename TY>
 void launch_bwd(const NormBwdParams& p, hipStream_t stream) {
-  const uint32_t grid = uint32_t(bwd_grid(p.M, p.d));
+  const uint32_t grid = uint32_t(bwd_grid(p.M, p.d, sizeof(TX)));
 #define AA_CALL(WPR, NC)                                                                              \
   launch((norm_bwd_kernel<TX, TY, WPR, NC>), dim3(grid), dim3(WPR == 1 ? kBwdWaves * 64 : WPR * 64),  \
          uint32_t(WPR == 1 && (p.sum_xh || p.sum_1) ? 8 * p.d : 0), stream, p)
-  AA_NORM_SPLIT(p.d, AA_CALL);
+  AA_NORM_SPLIT(p.d, AA_CALL, AA_CALL(8, 2));
 #undef AA_CALL
 }
 
@@ -422,12 +444,14 @@ aa_status_t launch_norm_fwd(const NormFwdCall& c, hipStream_t stream) {
   return after_launch(stream, "norm_fwd_kernel");
 }
 
-size_t norm_bwd_workspace_bytes(int64_t M, int64_t d) { return size_t(bwd_grid(M, d)) * 2 * size_t(d) * 4; }
+// For either type: bf16 rows have the larger grid.
+size_t norm_bwd_workspace_bytes(int64_t M, int64_t d) { return size_t(bwd_grid(M, d, 2)) * 2 * size_t(d) * 4; }
 
 aa_status_t launch_norm_bwd(const NormBwdCall& c, hipStream_t stream) {
   const bool sums = c.dgamma || c.dbeta;
   // a single workgroup's sums are the result
-  const bool direct = bwd_grid(c.M, c.d) == 1;
+  const int64_t grid = bwd_grid(c.M, c.d, size_of(c.x_dtype));
+  const bool direct = grid == 1;
   const NormBwdParams p{c.X, c.dY, c.gamma, c.mean, c.rstd, c.dS, c.dX,
                         direct ? c.dgamma : sums ? c.workspace : nullptr,
                         direct ? c.dbeta : sums ? c.workspace + c.d : nullptr, c.M, c.d,
@@ -445,7 +469,7 @@ aa_status_t launch_norm_bwd(const NormBwdCall& c, hipStream_t stream) {
   }
   if (!sums) return AA_OK;
   launch(norm_bwd_reduce_kernel, dim3(uint32_t((2 * c.d + kCols - 1) / kCols)), dim3(1024), 0u, stream,
-         static_cast<const float*>(c.workspace), int(bwd_grid(c.M, c.d)), c.d, c.dgamma, c.dbeta);
+         static_cast<const float*>(c.workspace), int(grid), c.d, c.dgamma, c.dbeta);
   return after_launch(stream, "norm_bwd_reduce_kernel");
 }
 

@@ -293,6 +293,35 @@ def test_repeats_streams_and_graphs():
         assert all(torch.equal(a, b) for a, b in zip(o, ref))
 
 
+def test_offsets_beyond_32_bits():
+    """More than 2^31 elements: the last rows equal those of a call of their own
+    (a row does not depend on the others), rows of zeros add nothing."""
+    d, k = 16384, 3
+    M = (1 << 31) // d + 200
+    X, dY = (torch.zeros(M, d, dtype=BF16, device=DEV) for _ in range(2))
+    X[-k:], g = make(k, d, BF16, 12)
+    dY[-k:] = rand(g, (k, d), BF16)
+    gamma = rand(g, (d,), F32)
+    Y, dX = torch.empty_like(X), torch.empty_like(X)
+    mean, rstd = torch.empty(M, device=DEV), torch.empty(M, device=DEV)
+    dG, dB = torch.empty(d, device=DEV), torch.empty(d, device=DEV)
+    ws = torch.empty(aa.aa_layernorm_bwd_workspace(M, d), dtype=torch.uint8, device=DEV)
+    aa.aa_layernorm_fwd(X, gamma, None, Y, mean=mean, rstd=rstd)
+    aa.aa_layernorm_bwd(X, dY, gamma, mean, rstd, dX, dG, dB, None, ws)
+    x, dy = X[-k:].clone(), dY[-k:].clone()
+    y, dx, m, r = torch.empty_like(x), torch.empty_like(x), torch.empty(k, device=DEV), torch.empty(k, device=DEV)
+    aa.aa_layernorm_fwd(x, gamma, None, y, mean=m, rstd=r)
+    aa.aa_layernorm_bwd(x, dy, gamma, m, r, dx)
+    assert torch.equal(Y[-k:], y) and torch.equal(dX[-k:], dx) and torch.equal(mean[-k:], m)
+    assert torch.equal(rstd[-k:], r) and not bool(Y[:-k].any()) and not bool(dX[:-k].any())
+    # k terms, each two roundings (the deviation and its product with rstd) and one of the product
+    xh = (x.double() - m.double()[:, None]) * r.double()[:, None]
+    mag = (dy.double() * xh).abs().sum(0) + (dy.double().abs() * (x.double().abs() + m.double().abs()[:, None]) *
+                                             r.double()[:, None]).sum(0)
+    close(dG, (dy.double() * xh).sum(0).cpu(), ((k + 3) * U * mag).cpu(), "dgamma")
+    close(dB, dy.double().sum(0).cpu(), (k * U * dy.double().abs().sum(0)).cpu(), "dbeta")
+
+
 def test_binding_refuses_before_the_library():
     X, Y = torch.zeros(4, 8, device=DEV), torch.zeros(4, 8, device=DEV)
     with pytest.raises(ValueError, match="contiguous"):
