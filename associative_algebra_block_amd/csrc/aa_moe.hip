@@ -10,7 +10,11 @@
 // call is reading those blocks (9.1 MB for one token of the 2048 -> 768
 // experts at q = 16 with 8 chosen) at a latency that few tokens do not hide,
 // so every kernel spreads its loads over as many waves as there are 16-column
-// strips and issues them before the first use.
+// strips and issues them before the first use.  One token takes 4.0 + 6.2 + 4.3
+// us (logits, gate and up, down), each within a few us of an empty launch;
+// sixteen, 120 MB, 4.9 + 19.1 + 11.9 us: 4 TB/s over the last two, where a plain
+// read of as much reaches 6.8; the choice in front of the loads and the tails
+// take the rest.
 //
 // Three launches: the logits; gate and up of every (token, expert) pair; the
 // down projection with the weighted sum.  The choice itself is no launch: each
@@ -19,6 +23,8 @@
 // bf16 values are exact and their sum all but exact, so the order of summation
 // never decides between two experts.  The hidden activation stays float32.
 #include <hip/hip_runtime.h>
+
+#include <algorithm>
 
 #include "aa_device.h"
 #include "aa_internal.h"
@@ -68,7 +74,7 @@ __global__ __launch_bounds__(256) void moe_router_kernel(MoeParams p) {
     const u32x4_t a = *reinterpret_cast<const u32x4_t*>(x + c);
     const u32x4_t b = *reinterpret_cast<const u32x4_t*>(w + c);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {   // a product of two bf16 is exact in float32
+    for (int j = 0; j < 4; ++j) {   // a product of two bf16 that does not overflow is exact in float32
       acc += double(lo_f(a[j]) * lo_f(b[j]));
       acc += double(hi_f(a[j]) * hi_f(b[j]));
     }
@@ -336,7 +342,10 @@ __global__ __launch_bounds__(256) void moe_down_kernel(MoeParams p) {
   const float* weight = p.share + t * p.top_k;
   const int steps = p.top_k * groups.n * ((bi + 31) / 32);
   float acc[NS] = {};
-  strip_dot<NS>(W, [&](int a) { return int64_t(chosen[a]) * p.D * p.F; }, p.h + t * p.top_k * p.F, int(p.F),
+  // the place is held inside the weights even where a caller lets another call
+  // or kernel write the workspace meanwhile: wrong values then, but no fault
+  const uint32_t last_expert = uint32_t(p.E - 1);
+  strip_dot<NS>(W, [&](int a) { return int64_t(min(uint32_t(chosen[a]), last_expert)) * p.D * p.F; }, p.h + t * p.top_k * p.F, int(p.F),
                 [&](int a) { return weight[a]; }, groups, k, p.q, bi, int64_t(bi) * bo, strip, lane, wave * steps / 4,
                 (wave + 1) * steps / 4, acc);
 #pragma unroll
@@ -408,13 +417,28 @@ aa_status_t launch_moe(const aa_plan_s& up, const aa_plan_s& down, const MoeCall
   if (st != AA_OK) return st;
   const uint32_t strips = uint32_t(p.F / 16), lds = uint32_t(p.E * 16);
   const dim3 block(kUpThreads);
-  if (pairs * strips <= 1024) launch((moe_up_kernel<4>), dim3((strips + 1) / 2, pairs), block, lds, stream, p);
-  else if (pairs * strips <= 2048) launch((moe_up_kernel<2>), dim3((strips + 3) / 4, pairs), block, lds, stream, p);
-  else launch((moe_up_kernel<1>), dim3((strips + 7) / 8, pairs), block, lds, stream, p);
+  // Waves a strip: as many as repay their join.  Measured with 1, 2 and 4 (us of
+  // the whole call): sums of 8 steps of 32 rows (q = 16, 2048 -> 768) at 384 strips
+  // 14.1, 13.1, 12.7; at 768 15.1, 14.6, 15.6; at 1152 16.4, 17.3, 17.6.  Of 16 and
+  // more steps (q = 4, 1024 -> 512) at 512 strips 16.5, 14.5, 13.4; at 2048 21.4,
+  // 20.2, 22.5; (24 steps, Q2 x Q2, 768 -> 2048) at 5120 38.3, 36.1, 42.3;
+  // at 20480 79.8 with one wave and 91.5 with two.
+  const int groups = up.law == AA_LAW_Q2XQ2 ? 4 : std::min(int(up.q), 2);
+  const bool long_sums = groups * (up.d_in / up.q) >= 16 * 32;
+  const uint64_t all_strips = uint64_t(pairs) * strips;
+  if (all_strips <= (long_sums ? 1536 : 512))
+    launch((moe_up_kernel<4>), dim3((strips + 1) / 2, pairs), block, lds, stream, p);
+  else if (all_strips <= (long_sums ? 8192 : 1024))
+    launch((moe_up_kernel<2>), dim3((strips + 3) / 4, pairs), block, lds, stream, p);
+  else
+    launch((moe_up_kernel<1>), dim3((strips + 7) / 8, pairs), block, lds, stream, p);
   st = after_launch(stream, "moe_up_kernel");
   if (st != AA_OK) return st;
   const uint32_t out_strips = uint32_t(p.D / 16), q = uint32_t(p.q);
-  if (M * out_strips < 1024) launch((moe_down_kernel<1>), dim3(out_strips, M), dim3(256), 0u, stream, p);
+  // Two strips a workgroup share the hidden activation's loads, where there are
+  // enough of them: 5 tokens of Q2 x Q2 experts (240 strips) take 21.7 us with one
+  // and 23.9 with two, 20 tokens (960) 38.2 and 36.1, 40 tokens 55.0 and 50.3.
+  if (uint64_t(M) * out_strips < 1024) launch((moe_down_kernel<1>), dim3(out_strips, M), dim3(256), 0u, stream, p);
   else launch((moe_down_kernel<2>), dim3((out_strips / q + 1) / 2 * q, M), dim3(256), 0u, stream, p);
   return after_launch(stream, "moe_down_kernel");
 }

@@ -347,8 +347,9 @@ aa_status_t aa_attn_decode(const void* Q, int64_t ldq, aa_dtype_t q_dtype, const
  * kept in float32 whatever up's out_dtype.  Rows whose explicit type lies
  * outside [0, q) are not written in any output.  A NaN logit is chosen first
  * and makes the token's weights NaN.  Limits: n_experts <= 512, top_k <= 64,
- * M * top_k <= 65535, D and F below 2^24; every (token, expert) pair reads its weights for itself,
- * so many tokens are better served expert by expert with aa_swiglu_ffn_fwd.
+ * M * top_k <= 65535, D and F below 2^24; every (token, expert) pair reads its
+ * weights for itself, so many tokens are better served expert by expert with
+ * aa_swiglu_ffn_fwd.
  * Workspace: at least what aa_moe_ffn_workspace reports; its contents are
  * overwritten, and calls that share one must not overlap in time.  M == 0 is
  * a no-op. */

@@ -161,6 +161,20 @@ def test_a_token_of_nan_stays_alone():
     assert bad[1][2].tolist() == [0, 1]
 
 
+def test_the_most_pairs_equal_parts_of_them():
+    """65535 (token, expert) pairs in one call give what 15 calls give; the last
+    tokens also against the definition."""
+    L = Layer("Qq", 2, 64, 32, 3, 19)
+    M, part = 65535, 4369
+    X = inp.gaussian((M, 64), 5, 1.0, BF16, DEV)
+    all_at_once = L.run(X, 1, False, 1)
+    parts = [L.run(X[lo:lo + part], 1, False, 1 + lo) for lo in range(0, M, part)]
+    for i, t in enumerate(all_at_once):
+        assert torch.equal(t, torch.cat([p[i] for p in parts]))
+    last = slice(M - 9, M)
+    L.check(X[last], 1, False, oracle.types_pos_mod(9, 2, 1 + M - 9), *(t[last] for t in all_at_once))
+
+
 def test_one_expert_is_the_ffn():
     """One expert with weight one is aa_swiglu_ffn_fwd, which rounds the hidden
     activation to bf16 (2^-9 of each, in quadrature well below 2^-8 of y)."""
