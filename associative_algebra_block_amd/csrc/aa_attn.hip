@@ -38,8 +38,8 @@ namespace {
 
 constexpr int kKeys = 32;        // keys of one step of a wave
 constexpr int kAttnWaves = 4;
-constexpr int kMinTiles = 8;     // steps of a workgroup below which a sequence is never split further
-constexpr int kFullTiles = 32;   // steps that repay a workgroup's start and join
+constexpr int kMinTiles = 4;     // steps of a part that a sequence is split into at the least, one a wave
+constexpr int kFullTiles = 32;   // steps that repay a workgroup's start and join where others wait for the place
 constexpr int kMaxSplit = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -534,27 +534,36 @@ void launch_attn_dc(const AttnParams& p, bool q_f32, uint32_t grid, hipStream_t 
 
 }  // namespace
 
-// Parts that one (sequence, kv head, head tile) is split into at most: four
-// workgroups a compute unit when every page of the table is in use, eight
-// where several sequences may differ in length, as long as each part keeps
-// kMinTiles steps.  A shorter sequence takes parts of the same size, kFullTiles
-// at most, and then fewer of them (split_tiles).  Measured on 32 sequences of
-// 1000 to 8192 positions with 8 kv heads of 128, 16 to a page: 8 a unit
-// 100.3 us, 4 a unit 102.8 us; one sequence of 131001: 93.0 and 89.8 us.
-int attn_nsplit(int64_t n_seqs, int H, int Hkv, int64_t max_pages, int page) {
+// Parts that one (sequence, kv head, head tile) is split into at most: what
+// gives every compute unit a workgroup when every page of the table is in use,
+// as long as each part keeps kMinTiles steps; of narrow heads, whose small steps
+// are bound by latency, as many workgroups as fit, in parts of twice as many
+// steps.  More, up to eight workgroups a unit in parts of kFullTiles steps, even
+// out long sequences of different lengths.  A
+// shorter sequence takes parts of the same size, kFullTiles at most, and then
+// fewer of them (split_tiles).  Measured with 32 query and 8 kv heads of 128
+// (us): one sequence of 8000 in 16, 32, 64 parts 14.4, 12.3, 12.3; two of up to
+// 8000 in 8, 16, 32 parts 20.7, 15.9, 17.2; 32 of up to 2000 in 1, 2, 8 parts
+// 31.9, 35.3, 40.0 (31 of 100 with one of 2000 in 1 and 8: 27.1 and 19.0); 32 of
+// 1000 to 8192 in 4 and 8 parts 102.8 and 100.3; one of 2000 in parts of at least
+// 4 and 8 steps 9.3 and 11.0.  32 heads of 24, eight sequences of up to 1500 in
+// 1, 2, 4, 8 parts: 13.8, 14.5, 13.7, 13.4; four: 13.8, 11.9, 10.4, 10.4.
+int attn_nsplit(int64_t n_seqs, int H, int Hkv, int D, int64_t max_pages, int page) {
   const int64_t rows = std::max<int64_t>(n_seqs * Hkv * head_tiles_of(H / Hkv), 1);
   const int64_t tiles = (max_pages * page + kKeys - 1) / kKeys;
-  const int64_t want = ((n_seqs > 1 ? 8 : 4) * int64_t(device_cu_count()) + rows - 1) / rows;
-  return int(std::max<int64_t>(1, std::min<int64_t>({want, tiles / kMinTiles, kMaxSplit})));
+  if (tiles <= 4 * kMinTiles) return 1;   // 400 positions: 10.3 us, in two parts and a join 10.7
+  const int64_t units = device_cu_count(), per_unit = D <= 32 ? 8 : D <= 64 ? 4 : 1;
+  auto parts = [&](int64_t wgs_per_unit, int64_t steps) {   // rounded up: parts of at most `steps`
+    return std::min((wgs_per_unit * units + rows - 1) / rows, (tiles + steps - 1) / steps);
+  };
+  const int64_t fill = std::max(parts(1, kMinTiles), parts(per_unit, 2 * kMinTiles));
+  const int64_t even = tiles < 4 * kFullTiles ? 1 : parts(8, kFullTiles);
+  return int(std::max<int64_t>(1, std::min<int64_t>(std::max(fill, even), kMaxSplit)));
 }
 
 size_t attn_workspace_bytes(int64_t n_seqs, int H, int Hkv, int D, int page, int64_t max_pages) {
-  const int ns = attn_nsplit(n_seqs, H, Hkv, max_pages, page);
+  const int ns = attn_nsplit(n_seqs, H, Hkv, D, max_pages, page);
   return ns == 1 ? 0 : size_t(n_seqs) * size_t(H) * size_t(ns) * size_t(D + 2) * 4;
-}
-
-int64_t attn_workgroups(int64_t n_seqs, int H, int Hkv, int page, int64_t max_pages) {
-  return n_seqs * Hkv * head_tiles_of(H / Hkv) * attn_nsplit(n_seqs, H, Hkv, max_pages, page);
 }
 
 aa_status_t launch_attn_decode(const AttnCall& c, hipStream_t stream) {
@@ -575,14 +584,14 @@ aa_status_t launch_attn_decode(const AttnCall& c, hipStream_t stream) {
   p.D = c.head_dim;
   p.head_tiles = head_tiles_of(p.G);
   p.page_shift = page_shift_of(c.page_size);
-  p.nsplit = attn_nsplit(c.n_seqs, c.n_heads, c.n_kv_heads, c.max_pages, c.page_size);
+  p.nsplit = attn_nsplit(c.n_seqs, c.n_heads, c.n_kv_heads, c.head_dim, c.max_pages, c.page_size);
   const int64_t tiles = (c.max_pages * c.page_size + kKeys - 1) / kKeys;
   p.min_tiles = int(std::min<int64_t>(std::max<int64_t>(tiles / p.nsplit, kMinTiles), kFullTiles));
   p.o_f32 = c.o_dtype == AA_F32;
   p.scale = c.scale;
   p.part = static_cast<float*>(c.workspace);
   p.ml = p.part ? p.part + int64_t(p.B) * p.H * p.nsplit * p.D : nullptr;
-  const uint32_t grid = uint32_t(attn_workgroups(c.n_seqs, c.n_heads, c.n_kv_heads, c.page_size, c.max_pages));
+  const uint32_t grid = uint32_t(c.n_seqs * c.n_kv_heads * p.head_tiles * p.nsplit);
   const bool q_f32 = c.q_dtype == AA_F32;
   switch ((p.D + 31) / 32) {
     case 1: launch_attn_dc<1>(p, q_f32, grid, stream); break;

@@ -240,7 +240,51 @@ def test_offsets_beyond_32_bits():
     assert torch.equal(c.V[pg, :, :, 999 % page], kv[0, Hkv * D:].view(Hkv, D).to(BF16))
 
 
+def test_more_than_65535_sequences():
+    """Pages shared between sequences, as after a common prompt."""
+    B, H, D, page, n_pages, scale = 70000, 2, 8, 16, 64, 0.5
+    g = torch.Generator().manual_seed(6)
+    K = torch.randn(n_pages, 1, page, D, generator=g).to(BF16).to(DEV)
+    V = torch.randn(n_pages, 1, D, page, generator=g).to(BF16).to(DEV)
+    table = torch.randint(0, n_pages, (B, 2), generator=g, dtype=torch.int32).to(DEV)
+    lens = torch.randint(0, 2 * page + 1, (B,), generator=g, dtype=torch.int32).to(DEV)
+    Q = queries(B, H, D, BF16, 3)
+    O = torch.full((B, H, D), 77.0, device=DEV)
+    aa.aa_attn_decode(Q, K, V, table, lens, O, scale)
+    k = K[table.long(), 0].double().reshape(B, 1, 2 * page, D)
+    v = V[table.long(), 0].double().transpose(2, 3).reshape(B, 1, 2 * page, D)
+    qk = k * Q.view(B, H, 1, D).double()
+    dead = (torch.arange(2 * page, device=DEV) >= lens[:, None])[:, None]
+    s = (qk.sum(3) * scale).masked_fill(dead, -float("inf"))
+    p = torch.softmax(s, 2).nan_to_num(0.0)
+    ref = (p[..., None] * v).sum(2)
+    # the bound of check(), of every sequence at once
+    mag = (qk.abs().sum(3) * scale).masked_fill(dead, 0.0).amax(2)
+    spread = s.amax(2) - s.masked_fill(dead, float("inf")).amin(2)
+    eps_s = (3 * D + 3) * U * mag + 8 * U * (1 + spread.clamp_min(0.0))
+    tol = (2 * eps_s + 2.0 ** -25 + 2 * (2 * page / 8 + 64) * U)[..., None] * (p[..., None] * v.abs()).sum(2)
+    tol = tol + U * (ref.abs() + tol)
+    assert bool(((O.double() - ref).abs() <= tol).all())
+
+
 # ------------------------------------------------------------------- append ---
+
+def test_append_of_a_long_prompt():
+    """More values than the threads of one launch."""
+    n, Hkv, D, page = 70000, 2, 128, 64
+    pages = -(-n // page)
+    g = torch.Generator().manual_seed(8)
+    kv = torch.randn(n, 2 * Hkv * D, generator=g).to(BF16).to(DEV)
+    table = torch.randperm(pages, generator=g).to(torch.int32)[None].to(DEV)
+    K = torch.zeros(pages, Hkv, page, D, dtype=BF16, device=DEV)
+    V = torch.zeros(pages, Hkv, D, page, dtype=BF16, device=DEV)
+    pos = torch.arange(n, dtype=torch.int32, device=DEV)
+    aa.aa_kv_append(kv[:, :Hkv * D], kv[:, Hkv * D:], K, V, table, pos, torch.zeros_like(pos))
+    gotK = K[table[0].long()].permute(0, 2, 1, 3).reshape(-1, Hkv * D)
+    gotV = V[table[0].long()].permute(0, 3, 1, 2).reshape(-1, Hkv * D)
+    assert torch.equal(gotK[:n], kv[:, :Hkv * D]) and torch.equal(gotV[:n], kv[:, Hkv * D:])
+    assert not bool(gotK[n:].any()) and not bool(gotV[n:].any())
+
 
 @pytest.mark.parametrize("Hkv,D,page,dt", [(32, 24, 64, F32), (1, 8, 16, BF16), (8, 128, 32, BF16), (3, 256, 16, F32)])
 def test_append_prompts_then_tokens(Hkv, D, page, dt):
