@@ -189,36 +189,41 @@ __device__ inline float quad_sum(float v) {   // over the four lanes of a column
   return v + __shfl_xor(v, 32, 64);
 }
 
-// places[e] += how many experts o come before e in the choice, over this
-// thread's share of the o; keys in LDS.  By the keys' upper halves alone
-// (exact == false) experts that agree in them get the same place, which the
-// caller sees: two such logits differ by less than 2^-20 of themselves.
+// How many experts come before expert e in the choice, where `per` neighbouring
+// lanes share an expert and take the others in turn, four at a time; keys in LDS,
+// zeros behind the last.  By the keys' upper halves alone (exact == false)
+// experts that agree in them get the same place, which the caller sees: two such
+// logits differ by less than 2^-20 of themselves.
 constexpr int kUpWaves = 8, kUpThreads = 64 * kUpWaves;
+static_assert(kUpThreads >= kMoeMaxExperts, "a thread for every expert");
 template <bool exact>
-__device__ inline void rank_experts(const uint64_t* keys, const uint32_t* upper, int E, int* places) {
-  const int per = E <= 64 ? 8 : E <= 128 ? 4 : E <= 256 ? 2 : 1;   // threads that share an expert's comparisons
-  const int width = kUpThreads / per, part = threadIdx.x / width;
-  const int begin = part * E / per, end = (part + 1) * E / per;
-  for (int e = threadIdx.x & (width - 1); e < E; e += width) {
-    const uint64_t mine = keys[e];
-    const uint32_t mine_upper = upper[e];
-    int r = 0;
-#pragma unroll 16
-    for (int o = begin; o < end; ++o) {
-      if constexpr (exact) r += keys[o] > mine || (keys[o] == mine && o < e) ? 1 : 0;
-      else r += upper[o] > mine_upper ? 1 : 0;
+__device__ inline int place_of(const uint64_t* keys, const uint32_t* upper, int E, int e, int per) {
+  const int part = threadIdx.x & (per - 1);
+  const uint64_t mine = keys[e];
+  const uint32_t mine_upper = uint32_t(mine >> 32);
+  int r = 0;
+#pragma unroll 4
+  for (int o = 4 * part; o < E; o += 4 * per) {
+    if constexpr (exact) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r += keys[o + j] > mine || (keys[o + j] == mine && o + j < e) ? 1 : 0;
+    } else {
+      const u32x4_t u = *reinterpret_cast<const u32x4_t*>(upper + o);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) r += u[j] > mine_upper ? 1 : 0;
     }
-    atomicAdd(&places[e], r);
   }
+  for (int s = 1; s < per; s *= 2) r += __shfl_xor(r, s, 64);
+  return r;
 }
 
 // Gate, up and SiLU of one (token, rank): WS waves per 16 hidden columns, which
 // share the sum's parts and join in LDS.
 template <int WS>
 __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(MoeParams p) {
-  extern __shared__ uint64_t s_key[];   // [E], then [E] upper halves and [E] places
-  uint32_t* s_upper = reinterpret_cast<uint32_t*>(s_key + p.E);
-  int* s_place = reinterpret_cast<int*>(s_upper + p.E);
+  __shared__ uint64_t s_key[kMoeMaxExperts];
+  __shared__ __align__(16) uint32_t s_upper[kMoeMaxExperts];
+  __shared__ int s_place[kMoeMaxExperts];
   __shared__ int s_expert, s_hits[3];
   __shared__ uint64_t s_top;
   __shared__ float s_red[kUpWaves], s_part[kUpWaves][2][16];
@@ -233,35 +238,39 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(MoeParams p) {
   // halves are a fifth of the exact ones' work (which took 7 of 30 us with 16
   // tokens and 128 experts) and nearly always decide; where the first place,
   // this workgroup's or the border of the choice is shared, all are compared.
-  for (int e = threadIdx.x; e < p.E; e += kUpThreads) {
-    const uint64_t key = choice_key(p.logits[t * p.E + e]);
+  // The ranking takes 2 us of a call; where every wave searched the keys for its
+  // expert bit by bit, one token took 1.2 us longer.
+  {
+    const int e = threadIdx.x;
+    const uint64_t key = e < p.E ? choice_key(p.logits[t * p.E + e]) : 0;
     s_key[e] = key;
     s_upper[e] = uint32_t(key >> 32);
-    s_place[e] = 0;
+    if (e < 3) s_hits[e] = 0;
   }
-  if (threadIdx.x < 3) s_hits[threadIdx.x] = 0;
   __syncthreads();
-  rank_experts<false>(s_key, s_upper, p.E, s_place);
-  __syncthreads();
-  auto find = [&] {   // the experts at this workgroup's place and at the first
-    for (int e = threadIdx.x; e < p.E; e += kUpThreads) {
-      const int place = s_place[e];
-      if (place == 0) s_top = s_key[e], atomicAdd(&s_hits[0], 1);
-      if (place == rank) s_expert = e, atomicAdd(&s_hits[1], 1);
-      if (place < p.top_k) atomicAdd(&s_hits[2], 1);
-    }
+  const int per = p.E <= 64 ? 8 : p.E <= 128 ? 4 : p.E <= 256 ? 2 : 1;
+  const int e = threadIdx.x / uint32_t(per);
+  const bool first = (threadIdx.x & (per - 1)) == 0 && e < p.E;
+  auto settle = [&](int place) {   // the experts at this workgroup's place and at the first
+    if (first) s_place[e] = place;
+    if (first && place == 0) s_top = s_key[e], atomicAdd(&s_hits[0], 1);
+    if (first && place == rank) s_expert = e, atomicAdd(&s_hits[1], 1);
+    const int chosen = __popcll(__ballot(first && place < p.top_k));
+    if (lane == 0 && chosen) atomicAdd(&s_hits[2], chosen);
     __syncthreads();
   };
-  find();
+  settle(place_of<false>(s_key, s_upper, p.E, e, per));
   if (s_hits[0] != 1 || s_hits[1] != 1 || s_hits[2] != p.top_k) {   // the same for all threads
-    for (int e = threadIdx.x; e < p.E; e += kUpThreads) s_place[e] = 0;
-    __syncthreads();
-    rank_experts<true>(s_key, s_upper, p.E, s_place);
-    __syncthreads();
-    find();
+    const int place = place_of<true>(s_key, s_upper, p.E, e, per);
+    __syncthreads();                                                // the counts have been read
+    settle(place);
   }
   const int expert = __builtin_amdgcn_readfirstlane(s_expert);
-  if (blockIdx.x == 0) {   // this pair's weight, for the next kernel and the caller
+  // This pair's weight, for the next kernel and the caller.  In a workgroup of its
+  // own it takes 0.3 us less for one token, but with one workgroup more a pair
+  // those that read the same strip of an expert no longer fall on the same die
+  // (80 tokens of Q2 x Q2 experts: 106 instead of 77 us).
+  if (blockIdx.x == 0) {
     const uint64_t top_key = s_top;
     const double top = top_key == ~uint64_t(0) ? double(NAN)
                        : __longlong_as_double((long long)(top_key >> 63 ? top_key ^ uint64_t(1) << 63 : ~top_key));
@@ -415,7 +424,7 @@ aa_status_t launch_moe(const aa_plan_s& up, const aa_plan_s& down, const MoeCall
   launch(moe_router_kernel, dim3((p.E + 3) / 4, M), dim3(256), 0u, stream, p);
   aa_status_t st = after_launch(stream, "moe_router_kernel");
   if (st != AA_OK) return st;
-  const uint32_t strips = uint32_t(p.F / 16), lds = uint32_t(p.E * 16);
+  const uint32_t strips = uint32_t(p.F / 16);
   const dim3 block(kUpThreads);
   // Waves a strip: as many as repay their join.  Measured with 1, 2 and 4 (us of
   // the whole call): sums of 8 steps of 32 rows (q = 16, 2048 -> 768) at 384 strips
@@ -427,11 +436,11 @@ aa_status_t launch_moe(const aa_plan_s& up, const aa_plan_s& down, const MoeCall
   const bool long_sums = groups * (up.d_in / up.q) >= 16 * 32;
   const uint64_t all_strips = uint64_t(pairs) * strips;
   if (all_strips <= (long_sums ? 1536 : 512))
-    launch((moe_up_kernel<4>), dim3((strips + 1) / 2, pairs), block, lds, stream, p);
+    launch((moe_up_kernel<4>), dim3((strips + 1) / 2, pairs), block, 0u, stream, p);
   else if (all_strips <= (long_sums ? 8192 : 1024))
-    launch((moe_up_kernel<2>), dim3((strips + 3) / 4, pairs), block, lds, stream, p);
+    launch((moe_up_kernel<2>), dim3((strips + 3) / 4, pairs), block, 0u, stream, p);
   else
-    launch((moe_up_kernel<1>), dim3((strips + 7) / 8, pairs), block, lds, stream, p);
+    launch((moe_up_kernel<1>), dim3((strips + 7) / 8, pairs), block, 0u, stream, p);
   st = after_launch(stream, "moe_up_kernel");
   if (st != AA_OK) return st;
   const uint32_t out_strips = uint32_t(p.D / 16), q = uint32_t(p.q);
