@@ -49,6 +49,7 @@ struct MoeParams {
   int64_t D, F;
   int32_t E, top_k, q, law, normalize, y_f32;
   int32_t off;           // position of token 0, modulo q
+  uint32_t parts, pairs; // workgroups of a pair, (token, expert) pairs: the second kernel
 };
 
 // The row type of token t; rows of a type outside [0, q) are left alone.  A
@@ -227,9 +228,21 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(MoeParams p) {
   __shared__ int s_expert, s_hits[3];
   __shared__ uint64_t s_top;
   __shared__ float s_red[kUpWaves], s_part[kUpWaves][2][16];
-  const int64_t pair = blockIdx.y;
-  const int64_t t = blockIdx.y / uint32_t(p.top_k);
-  const int rank = int(pair - t * p.top_k);
+  // Workgroup `part` of a pair.  Consecutive workgroups go to the eight dies in
+  // turn: where a pair has a multiple of eight, those of a strip lie on one die,
+  // and pairs that share an expert meet there.  Where it has not, a row of the
+  // grid is eight pairs, and each die takes all workgroups of an eighth of the
+  // parts (q = 2, 2048 -> 768, 16 tokens: 56 against 61 us; with 16 parts, where
+  // both do it, 83 against 77).
+  uint32_t part = blockIdx.x, pair = blockIdx.y;
+  if (gridDim.x != p.parts) {
+    const uint32_t place = blockIdx.x % 8 * p.parts + blockIdx.x / 8;
+    part = place / 8;
+    pair = blockIdx.y * 8 + place % 8;
+    if (pair >= p.pairs) return;
+  }
+  const int64_t t = pair / uint32_t(p.top_k);
+  const int rank = int(pair) - int(t) * p.top_k;
   const int tau = row_type(p, int(t));
   if (tau < 0 || tau >= p.q) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -270,7 +283,7 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(MoeParams p) {
   // own it takes 0.3 us less for one token, but with one workgroup more a pair
   // those that read the same strip of an expert no longer fall on the same die
   // (80 tokens of Q2 x Q2 experts: 106 instead of 77 us).
-  if (blockIdx.x == 0) {
+  if (part == 0) {
     const uint64_t top_key = s_top;
     const double top = top_key == ~uint64_t(0) ? double(NAN)
                        : __longlong_as_double((long long)(top_key >> 63 ? top_key ^ uint64_t(1) << 63 : ~top_key));
@@ -298,7 +311,7 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(MoeParams p) {
 
   const int bi = int(uint32_t(p.D) / uint32_t(p.q)), bo = int(uint32_t(p.F) / uint32_t(p.q));
   const int strips = bo / 16;
-  const int s = blockIdx.x * (kUpWaves / WS) + wave / WS;   // strip of the whole hidden row
+  const int s = int(part) * (kUpWaves / WS) + wave / WS;   // strip of the whole hidden row
   const bool live = s < p.q * strips;
   const int k = s / strips, strip = s - k * strips;
   float acc[2] = {0.0f, 0.0f};
@@ -324,7 +337,7 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(MoeParams p) {
       u += s_part[wave + v][1][lane & 15];
     }
   }
-  if (live && lane < 16) p.h[pair * p.F + int64_t(k) * bo + strip * 16 + lane] = g / (1.0f + expf(-g)) * u;
+  if (live && lane < 16) p.h[int64_t(pair) * p.F + int64_t(k) * bo + strip * 16 + lane] = g / (1.0f + expf(-g)) * u;
 }
 
 // Down projection and weighted sum: a workgroup per NS strips of 16 output
@@ -435,12 +448,13 @@ aa_status_t launch_moe(const aa_plan_s& up, const aa_plan_s& down, const MoeCall
   const int groups = up.law == AA_LAW_Q2XQ2 ? 4 : std::min(int(up.q), 2);
   const bool long_sums = groups * (up.d_in / up.q) >= 16 * 32;
   const uint64_t all_strips = uint64_t(pairs) * strips;
-  if (all_strips <= (long_sums ? 1536 : 512))
-    launch((moe_up_kernel<4>), dim3((strips + 1) / 2, pairs), block, 0u, stream, p);
-  else if (all_strips <= (long_sums ? 8192 : 1024))
-    launch((moe_up_kernel<2>), dim3((strips + 3) / 4, pairs), block, 0u, stream, p);
-  else
-    launch((moe_up_kernel<1>), dim3((strips + 7) / 8, pairs), block, 0u, stream, p);
+  const int ws_up = all_strips <= (long_sums ? 1536 : 512) ? 4 : all_strips <= (long_sums ? 8192 : 1024) ? 2 : 1;
+  p.parts = (strips * ws_up + kUpWaves - 1) / kUpWaves;
+  p.pairs = pairs;
+  const dim3 grid = p.parts % 8 && pairs >= 64 ? dim3(8 * p.parts, (pairs + 7) / 8) : dim3(p.parts, pairs);
+  if (ws_up == 4) launch((moe_up_kernel<4>), grid, block, 0u, stream, p);
+  else if (ws_up == 2) launch((moe_up_kernel<2>), grid, block, 0u, stream, p);
+  else launch((moe_up_kernel<1>), grid, block, 0u, stream, p);
   st = after_launch(stream, "moe_up_kernel");
   if (st != AA_OK) return st;
   const uint32_t out_strips = uint32_t(p.D / 16), q = uint32_t(p.q);

@@ -100,6 +100,8 @@ CASES = [  # law, q, D, F, E, top_k, M, normalize, out, pos
     ("Qq", 4, 64, 64, 300, 7, 3, True, "f32", 3),
     ("Qq", 2, 1024, 2080, 3, 2, 2, True, "f32", 1),          # wide blocks: several rounds of loads
     ("Qq", 8, 128, 128, 9, 1, 33, False, "f32", 100),
+    ("Qq", 4, 64, 320, 6, 3, 30, True, "f32", 1),            # 90 pairs in rows of eight, three workgroups each
+    ("Qq", 2, 64, 160, 6, 3, 30, False, "bf16", 0),
 ]
 
 
