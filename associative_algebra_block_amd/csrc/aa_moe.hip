@@ -342,12 +342,12 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(MoeParams p) {
 
 // Down projection and weighted sum: a workgroup per NS strips of 16 output
 // columns of a token (NS = 2: neighbours of one output group, which share the
-// loads of the hidden activation; the last of an odd number is alone).  Its
-// four waves share the parts of the sum over the chosen experts and join in a
-// fixed order.
-template <int NS>
-__global__ __launch_bounds__(256) void moe_down_kernel(MoeParams p) {
-  __shared__ float s_part[4][NS][16];
+// loads of the hidden activation; the last of an odd number is alone).  Its NW
+// waves share the parts of the sum over the chosen experts and join in a fixed
+// order.
+template <int NS, int NW>
+__global__ __launch_bounds__(64 * NW) void moe_down_kernel(MoeParams p) {
+  __shared__ float s_part[NW][NS][16];
   const int64_t t = blockIdx.y;
   const int tau = row_type(p, int(t));
   if (tau < 0 || tau >= p.q) return;
@@ -368,8 +368,8 @@ __global__ __launch_bounds__(256) void moe_down_kernel(MoeParams p) {
   // or kernel write the workspace meanwhile: wrong values then, but no fault
   const uint32_t last_expert = uint32_t(p.E - 1);
   strip_dot<NS>(W, [&](int a) { return int64_t(min(uint32_t(chosen[a]), last_expert)) * p.D * p.F; }, p.h + t * p.top_k * p.F, int(p.F),
-                [&](int a) { return weight[a]; }, groups, k, p.q, bi, int64_t(bi) * bo, strip, lane, wave * steps / 4,
-                (wave + 1) * steps / 4, acc);
+                [&](int a) { return weight[a]; }, groups, k, p.q, bi, int64_t(bi) * bo, strip, lane, wave * steps / NW,
+                (wave + 1) * steps / NW, acc);
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
     const float y = quad_sum(acc[i]);
@@ -378,7 +378,10 @@ __global__ __launch_bounds__(256) void moe_down_kernel(MoeParams p) {
   __syncthreads();
   const int i = threadIdx.x / 16, c = threadIdx.x & 15;
   if (i < NS && strip + i < strips) {
-    const float v = (s_part[0][i][c] + s_part[1][i][c]) + (s_part[2][i][c] + s_part[3][i][c]);
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW; w += 4)
+      v += (s_part[w][i][c] + s_part[w + 1][i][c]) + (s_part[w + 2][i][c] + s_part[w + 3][i][c]);
     const int64_t at = t * p.D + int64_t(k) * bo + (strip + i) * 16 + c;
     if (p.y_f32) static_cast<float*>(p.Y)[at] = v;
     else static_cast<__bf16*>(p.Y)[at] = (__bf16)v;
@@ -439,30 +442,40 @@ aa_status_t launch_moe(const aa_plan_s& up, const aa_plan_s& down, const MoeCall
   if (st != AA_OK) return st;
   const uint32_t strips = uint32_t(p.F / 16);
   const dim3 block(kUpThreads);
-  // Waves a strip: as many as repay their join.  Measured with 1, 2 and 4 (us of
-  // the whole call): sums of 8 steps of 32 rows (q = 16, 2048 -> 768) at 384 strips
-  // 14.1, 13.1, 12.7; at 768 15.1, 14.6, 15.6; at 1152 16.4, 17.3, 17.6.  Of 16 and
-  // more steps (q = 4, 1024 -> 512) at 512 strips 16.5, 14.5, 13.4; at 2048 21.4,
-  // 20.2, 22.5; (24 steps, Q2 x Q2, 768 -> 2048) at 5120 38.3, 36.1, 42.3;
-  // at 20480 79.8 with one wave and 91.5 with two.
+  // Waves a strip: as many as repay their join.  Measured (us of the whole call)
+  // with 1, 2, 4 and 8, for sums of 8 steps of 32 rows (q = 16, 2048 -> 768) at 384
+  // strips 14.0, 13.2, 12.8, 14.1; at 768 15.5, 14.9, 15.5, 16.7; at 1536 17.2, 17.8,
+  // 17.9, 23.0.  For 16 and more steps (Q2 x Q2, 768 -> 2048) at 256 strips 19.1,
+  // 16.0, 14.8, 13.9; at 1280 20.6, 19.7, 18.8, 20.8; at 5120 44.3, 41.7, 47.6, 59.4;
+  // at 10240 48.3, 53.0, 64.8, 90.1.
   const int groups = up.law == AA_LAW_Q2XQ2 ? 4 : std::min(int(up.q), 2);
   const bool long_sums = groups * (up.d_in / up.q) >= 16 * 32;
   const uint64_t all_strips = uint64_t(pairs) * strips;
-  const int ws_up = all_strips <= (long_sums ? 1536 : 512) ? 4 : all_strips <= (long_sums ? 8192 : 1024) ? 2 : 1;
+  const int ws_up = long_sums && all_strips <= 256 ? 8 : all_strips <= (long_sums ? 1536 : 512) ? 4
+                    : all_strips <= (long_sums ? 8192 : 1024) ? 2 : 1;
   p.parts = (strips * ws_up + kUpWaves - 1) / kUpWaves;
   p.pairs = pairs;
   const dim3 grid = p.parts % 8 && pairs >= 64 ? dim3(8 * p.parts, (pairs + 7) / 8) : dim3(p.parts, pairs);
-  if (ws_up == 4) launch((moe_up_kernel<4>), grid, block, 0u, stream, p);
+  if (ws_up == 8) launch((moe_up_kernel<8>), grid, block, 0u, stream, p);
+  else if (ws_up == 4) launch((moe_up_kernel<4>), grid, block, 0u, stream, p);
   else if (ws_up == 2) launch((moe_up_kernel<2>), grid, block, 0u, stream, p);
   else launch((moe_up_kernel<1>), grid, block, 0u, stream, p);
   st = after_launch(stream, "moe_up_kernel");
   if (st != AA_OK) return st;
   const uint32_t out_strips = uint32_t(p.D / 16), q = uint32_t(p.q);
-  // Two strips a workgroup share the hidden activation's loads, where there are
-  // enough of them: 5 tokens of Q2 x Q2 experts (240 strips) take 21.7 us with one
-  // and 23.9 with two, 20 tokens (960) 38.2 and 36.1, 40 tokens 55.0 and 50.3.
-  if (uint64_t(M) * out_strips < 1024) launch((moe_down_kernel<1>), dim3(out_strips, M), dim3(256), 0u, stream, p);
-  else launch((moe_down_kernel<2>), dim3((out_strips / q + 1) / 2 * q, M), dim3(256), 0u, stream, p);
+  // Two strips a workgroup, which share the hidden activation's loads, where there
+  // are enough of them, else one, with four or, for long sums, sixteen waves:
+  // (2 strips x 8 waves, 1 x 4, 1 x 16) take for 1, 5, 10 and 20 tokens of Q2 x Q2
+  // experts (48, 240, 480, 960 strips, 128 steps) 15.9, 16.2, 14.3; 20.9, 20.7, 18.7;
+  // 24.9, 26.7, 27.2; 33.2, 35.9, 42.1 us; for 2 and 16 tokens of q = 16, 2048 -> 768
+  // (256, 2048 strips, 32 steps) 14.8, 14.6, 16.2 and 32.1, 33.5, 60.5.
+  const int steps = p.top_k * groups * int((p.F / p.q + 31) / 32);
+  if (uint64_t(M) * out_strips >= 400)
+    launch((moe_down_kernel<2, 8>), dim3((out_strips / q + 1) / 2 * q, M), dim3(512), 0u, stream, p);
+  else if (steps <= 64)
+    launch((moe_down_kernel<1, 4>), dim3(out_strips, M), dim3(256), 0u, stream, p);
+  else
+    launch((moe_down_kernel<1, 16>), dim3(out_strips, M), dim3(1024), 0u, stream, p);
   return after_launch(stream, "moe_down_kernel");
 }
 
