@@ -10,9 +10,9 @@
 // call is reading those blocks (9.1 MB for one token of the 2048 -> 768
 // experts at q = 16 with 8 chosen) at a latency that few tokens do not hide,
 // so every kernel spreads its loads over as many waves as there are 16-column
-// strips and issues them before the first use.  One token takes 4.0 + 6.2 + 4.3
+// strips and issues them before the first use.  One token takes 4.0 + 6.0 + 4.0
 // us (logits, gate and up, down), each within a few us of an empty launch;
-// sixteen, 120 MB, 4.9 + 19.1 + 11.9 us: 4 TB/s over the last two, where a plain
+// sixteen, 120 MB, 4.7 + 18.3 + 11.4 us: 4 TB/s over the last two, where a plain
 // read of as much reaches 6.8; the choice in front of the loads and the tails
 // take the rest.
 //
@@ -468,9 +468,13 @@ aa_status_t launch_moe(const aa_plan_s& up, const aa_plan_s& down, const MoeCall
   // (2 strips x 8 waves, 1 x 4, 1 x 16) take for 1, 5, 10 and 20 tokens of Q2 x Q2
   // experts (48, 240, 480, 960 strips, 128 steps) 15.9, 16.2, 14.3; 20.9, 20.7, 18.7;
   // 24.9, 26.7, 27.2; 33.2, 35.9, 42.1 us; for 2 and 16 tokens of q = 16, 2048 -> 768
-  // (256, 2048 strips, 32 steps) 14.8, 14.6, 16.2 and 32.1, 33.5, 60.5.
+  // (256, 2048 strips, 32 steps) 14.8, 14.6, 16.2 and 32.1, 33.5, 60.5.  Short sums
+  // of very many strips do with four waves: 32 tokens (4096 strips) 51.9 and 53.0.
   const int steps = p.top_k * groups * int((p.F / p.q + 31) / 32);
-  if (uint64_t(M) * out_strips >= 400)
+  const uint64_t all_out = uint64_t(M) * out_strips;
+  if (all_out >= 1536 && steps <= 64)
+    launch((moe_down_kernel<2, 4>), dim3((out_strips / q + 1) / 2 * q, M), dim3(256), 0u, stream, p);
+  else if (all_out >= 400)
     launch((moe_down_kernel<2, 8>), dim3((out_strips / q + 1) / 2 * q, M), dim3(512), 0u, stream, p);
   else if (steps <= 64)
     launch((moe_down_kernel<1, 4>), dim3(out_strips, M), dim3(256), 0u, stream, p);

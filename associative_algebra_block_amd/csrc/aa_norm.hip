@@ -13,7 +13,7 @@
 // variance are two passes over registers (the variance is that of the
 // deviations, so a large common offset costs no digits), and every tensor
 // crosses HBM once.  All sums are float32.  12288 rows of 768 with a residual
-// operand (132 MB) take 20.7 us forward and 26.1 + 5.2 us backward, where a copy
+// operand (132 MB) take 20.8 us forward and 25.3 + 5.2 us backward, where a copy
 // of as many bytes takes 27; one row takes 2.8 us, which a launch costs anyhow.
 #include <hip/hip_runtime.h>
 
