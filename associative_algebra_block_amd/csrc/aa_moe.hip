@@ -367,7 +367,8 @@ __global__ __launch_bounds__(64 * NW) void moe_down_kernel(MoeParams p) {
   // the place is held inside the weights even where a caller lets another call
   // or kernel write the workspace meanwhile: wrong values then, but no fault
   const uint32_t last_expert = uint32_t(p.E - 1);
-  strip_dot<NS>(W, [&](int a) { return int64_t(min(uint32_t(chosen[a]), last_expert)) * p.D * p.F; }, p.h + t * p.top_k * p.F, int(p.F),
+  auto expert_at = [&](int a) { return int64_t(min(uint32_t(chosen[a]), last_expert)) * p.D * p.F; };
+  strip_dot<NS>(W, expert_at, p.h + t * p.top_k * p.F, int(p.F),
                 [&](int a) { return weight[a]; }, groups, k, p.q, bi, int64_t(bi) * bo, strip, lane, wave * steps / NW,
                 (wave + 1) * steps / NW, acc);
 #pragma unroll

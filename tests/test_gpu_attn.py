@@ -324,6 +324,50 @@ def test_append_prompts_then_tokens(Hkv, D, page, dt):
     assert torch.equal(c.K, wantK) and torch.equal(c.V, wantV)
 
 
+@pytest.mark.parametrize("Hkv,D,page,dt", [(3, 24, 16, F32), (2, 256, 128, BF16), (5, 8, 64, BF16), (1, 200, 32, F32)])
+def test_append_at_once_equals_append_in_parts(Hkv, D, page, dt):
+    """Prompts that begin at odd positions, padding, places outside the cache and
+    tokens in no order: what a call writes does not depend on how many tokens it
+    has, and nothing else changes."""
+    say("append in parts", Hkv, D, page, dt)
+    starts, lens = [5, 0, 1, 37, 64], [150, 200, 8, 97, 64]
+    lens[0] += 8 * D                                                       # enough for the call that turns
+    most = -(-max(s + n for s, n in zip(starts, lens)) // page)
+    g = torch.Generator().manual_seed(D)
+    pages = 5 * most + 3
+    table = torch.randperm(pages, generator=g)[:5 * most].to(torch.int32).view(5, most)
+    table[1, 1] = pages                                                    # no such page
+    seq = [s for s, n in enumerate(lens) for _ in range(n)]
+    pos = [b + j for b, n in zip(starts, lens) for j in range(n)]
+    seq, pos = torch.tensor(seq, dtype=torch.int32), torch.tensor(pos, dtype=torch.int32)
+    pos[40:43] = -1
+    pos[170] = most * page
+    seq[175], seq[176] = 5, -1
+    tail = torch.randperm(64, generator=g) + seq.numel() - 64              # the last prompt in no order
+    seq[-64:], pos[-64:] = seq[tail], pos[tail]
+    n, W = seq.numel(), Hkv * D
+    rows = torch.randn(n, 2 * W + 3, generator=g).to(dt).to(DEV)
+    k, v = rows[:, :W], rows[:, W:2 * W]
+    table, seq, pos = table.to(DEV), seq.to(DEV), pos.to(DEV)
+    K = [torch.full((pages, Hkv, page, D), 3.0, dtype=BF16, device=DEV) for _ in range(2)]
+    V = [torch.full((pages, Hkv, D, page), 3.0, dtype=BF16, device=DEV) for _ in range(2)]
+    aa.aa_kv_append(k, v, K[0], V[0], table, pos, seq)
+    for lo in range(0, n, 31):
+        aa.aa_kv_append(k[lo:lo + 31], v[lo:lo + 31], K[1], V[1], table, pos[lo:lo + 31], seq[lo:lo + 31])
+    assert torch.equal(K[0], K[1]) and torch.equal(V[0], V[1])
+    # and against plain indexing
+    ok = (pos >= 0) & (pos < most * page) & (seq >= 0) & (seq < 5)
+    t = ok.nonzero()[:, 0]
+    pg = table[seq[t].long(), pos[t].long() // page].long()
+    t, pg = t[pg < pages], pg[pg < pages]
+    slot = pos[t].long() % page
+    assert torch.equal(K[0][pg, :, slot], k[t].view(-1, Hkv, D).to(BF16))
+    assert torch.equal(V[0][pg, :, :, slot], v[t].view(-1, Hkv, D).to(BF16))
+    written = torch.zeros(pages, page, dtype=torch.bool, device=DEV)
+    written[pg, slot] = True
+    assert bool((K[0].transpose(1, 2)[~written] == 3).all()) and bool((V[0].permute(0, 3, 1, 2)[~written] == 3).all())
+
+
 def test_append_then_attend_equals_a_written_cache():
     lens = [1, 33, 100]
     H, Hkv, D = 8, 2, 64
