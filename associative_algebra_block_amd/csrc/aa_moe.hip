@@ -232,8 +232,8 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(MoeParams p) {
   // turn: where a pair has a multiple of eight, those of a strip lie on one die,
   // and pairs that share an expert meet there.  Where it has not, a row of the
   // grid is eight pairs, and each die takes all workgroups of an eighth of the
-  // parts (q = 2, 2048 -> 768, 16 tokens: 56 against 61 us; with 16 parts, where
-  // both do it, 83 against 77).
+  // parts (q = 2, 2048 -> 768, 16 tokens: 56 against 61 us; 640 -> 1440, 7 tokens,
+  // 42 pairs: 35 against 37; with 16 parts, where both do it, 83 against 77).
   uint32_t part = blockIdx.x, pair = blockIdx.y;
   if (gridDim.x != p.parts) {
     const uint32_t place = blockIdx.x % 8 * p.parts + blockIdx.x / 8;
@@ -456,7 +456,7 @@ aa_status_t launch_moe(const aa_plan_s& up, const aa_plan_s& down, const MoeCall
                     : all_strips <= (long_sums ? 8192 : 1024) ? 2 : 1;
   p.parts = (strips * ws_up + kUpWaves - 1) / kUpWaves;
   p.pairs = pairs;
-  const dim3 grid = p.parts % 8 && pairs >= 64 ? dim3(8 * p.parts, (pairs + 7) / 8) : dim3(p.parts, pairs);
+  const dim3 grid = p.parts % 8 && pairs >= 16 ? dim3(8 * p.parts, (pairs + 7) / 8) : dim3(p.parts, pairs);
   if (ws_up == 8) launch((moe_up_kernel<8>), grid, block, 0u, stream, p);
   else if (ws_up == 4) launch((moe_up_kernel<4>), grid, block, 0u, stream, p);
   else if (ws_up == 2) launch((moe_up_kernel<2>), grid, block, 0u, stream, p);
@@ -471,11 +471,13 @@ aa_status_t launch_moe(const aa_plan_s& up, const aa_plan_s& down, const MoeCall
   // 24.9, 26.7, 27.2; 33.2, 35.9, 42.1 us; for 2 and 16 tokens of q = 16, 2048 -> 768
   // (256, 2048 strips, 32 steps) 14.8, 14.6, 16.2 and 32.1, 33.5, 60.5.  Short sums
   // of very many strips do with four waves: 32 tokens (4096 strips) 51.9 and 53.0.
+  // Workgroups of 16 waves are one a unit, so more than 256 of them take two turns:
+  // q = 2, 640 -> 1440, 7 tokens (280 strips, 276 steps) 42 us, 2 x 8 37.
   const int steps = p.top_k * groups * int((p.F / p.q + 31) / 32);
   const uint64_t all_out = uint64_t(M) * out_strips;
   if (all_out >= 1536 && steps <= 64)
     launch((moe_down_kernel<2, 4>), dim3((out_strips / q + 1) / 2 * q, M), dim3(256), 0u, stream, p);
-  else if (all_out >= 400)
+  else if (all_out >= 400 || (steps > 64 && all_out > 256))
     launch((moe_down_kernel<2, 8>), dim3((out_strips / q + 1) / 2 * q, M), dim3(512), 0u, stream, p);
   else if (steps <= 64)
     launch((moe_down_kernel<1, 4>), dim3(out_strips, M), dim3(256), 0u, stream, p);
