@@ -32,6 +32,7 @@
 
 #include "aa_device.h"
 #include "aa_internal.h"
+#include "aa_rules.h"
 
 namespace aa {
 namespace {
@@ -536,7 +537,6 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendParams 
 // leave as 16 bytes a feature and 64 as whole lines; others leave one by one.
 // Rows of D + 2 values put the 64 reads of a wave (8 tokens apart, 8 features)
 // into different banks.
-constexpr int kTurnTokens = 64, kTurnThreads = 256;
 template <typename T>
 __global__ __launch_bounds__(kTurnThreads) void kv_append_turn_kernel(AppendParams p) {
   typedef __bf16 bf16x8_4 __attribute__((ext_vector_type(8), aligned(4)));
@@ -683,12 +683,8 @@ aa_status_t launch_kv_append(const AppendCall& c, hipStream_t stream) {
   AppendParams p{c.K,     c.V,        static_cast<__bf16*>(c.k_pages), static_cast<__bf16*>(c.v_pages),
                  c.page_table, c.seq, c.pos, c.ldk, c.ldv, c.n, c.n_seqs, c.n_pages, c.max_pages,
                  c.n * c.n_kv_heads * (c.head_dim / 8), c.n_kv_heads, c.head_dim, page_shift_of(c.page_size)};
-  // From about 8 D tokens on the turning repays its waits: with 8 heads of 128 and
-  // pages of 64, 512, 1024, 4096 and 40000 tokens of a prompt take 5.6, 8.7, 26 and
-  // 524 us one by one and 7.3, 7.7, 10.3 and 96 turned; with 32 heads of 24, 128, 256
-  // and 1024 take 3.3, 4.1, 8.4 and 3.9, 3.9, 4.6.  (A grid counts threads in 32 bits.)
-  if (p.n >= 8 * int64_t(p.D) && p.n < int64_t(1) << 30) {
-    const dim3 grid(uint32_t((p.n + kTurnTokens - 1) / kTurnTokens), uint32_t(p.Hkv));
+  if (append_turns(p.n, p.D)) {
+    const dim3 grid(uint32_t(append_turn_workgroups(p.n)), uint32_t(p.Hkv));
     const uint32_t lds = uint32_t(kTurnTokens * (p.D + 2) * 2);
     if (c.in_dtype == AA_F32) launch((kv_append_turn_kernel<float>), grid, dim3(kTurnThreads), lds, stream, p);
     else launch((kv_append_turn_kernel<__bf16>), grid, dim3(kTurnThreads), lds, stream, p);

@@ -368,6 +368,33 @@ def test_append_at_once_equals_append_in_parts(Hkv, D, page, dt):
     assert bool((K[0].transpose(1, 2)[~written] == 3).all()) and bool((V[0].permute(0, 3, 1, 2)[~written] == 3).all())
 
 
+@pytest.mark.parametrize("n", [(1 << 30) - 64, (1 << 30) - 63, (1 << 30) - 1])
+def test_append_of_the_most_tokens_of_a_grid(n):
+    """Around 2^30 tokens, where the turned append's threads reach what a grid
+    can count: the first tokens, one in the middle and the last are written, all
+    others are padding."""
+    say("append of many tokens", n)
+    D, page = 8, 16
+    rows = torch.zeros(n, D, dtype=BF16, device=DEV)            # keys and values alike
+    pos = torch.full((n,), -1, dtype=torch.int32, device=DEV)
+    seq = torch.zeros(n, dtype=torch.int32, device=DEV)
+    at = list(range(5)) + [n // 2 + 3, n - 2, n - 1]
+    for j, t in enumerate(at):
+        rows[t] = torch.arange(D, device=DEV) + 10 * (j + 1)
+        pos[t] = j + 12                                         # over a page's end
+    K = torch.full((4, 1, page, D), 3.0, dtype=BF16, device=DEV)
+    V = torch.full((4, 1, D, page), 3.0, dtype=BF16, device=DEV)
+    table = torch.tensor([[2, 1]], dtype=torch.int32, device=DEV)
+    wantK, wantV = K.clone(), V.clone()
+    for j, t in enumerate(at):
+        pg, slot = (2, 1)[(j + 12) // page], (j + 12) % page
+        wantK[pg, 0, slot] = rows[t]
+        wantV[pg, 0, :, slot] = rows[t]
+    aa.aa_kv_append(rows, rows, K, V, table, pos, seq)
+    torch.cuda.synchronize()
+    assert torch.equal(K, wantK) and torch.equal(V, wantV)
+
+
 def test_append_then_attend_equals_a_written_cache():
     lens = [1, 33, 100]
     H, Hkv, D = 8, 2, 64
