@@ -61,21 +61,24 @@ aa_status_t check_ld(int64_t ld, int64_t width, const char* what, const char* fn
   return AA_OK;
 }
 
-// A range of memory that a call writes, and one that it reads or writes.
+// A range of memory that a call reads or writes.  in_place: the index of the
+// output that this operand is, where the call replaces it in place.
 struct Range {
   const void* p;
   size_t bytes;
   const char* name;
+  int in_place = -1;
 };
 
-// No output may overlap another operand.  Empty and absent ranges overlap
-// nothing.  out[i] and all[j] that are the same operand (same name) are skipped.
-aa_status_t check_disjoint(const Range* out, int n_out, const Range* all, int n_all, const char* fn) {
-  for (int i = 0; i < n_out; ++i)
-    for (int j = 0; j < n_all; ++j) {
-      if (out[i].name == all[j].name || !out[i].p || !all[j].p || !out[i].bytes || !all[j].bytes) continue;
-      if (overlaps(out[i].p, out[i].bytes, all[j].p, all[j].bytes))
-        return fail(AA_ERR_INVALID_ARG, std::string(fn) + ": " + out[i].name + " overlaps " + all[j].name);
+// No output may overlap another operand; the outputs are the operands from
+// first_out on.  Empty and absent ranges overlap nothing.
+template <int N>
+aa_status_t check_disjoint(const Range (&all)[N], int first_out, const char* fn) {
+  for (int i = first_out; i < N; ++i)
+    for (int j = 0; j < N; ++j) {
+      if (j == i || all[j].in_place == i || !all[i].p || !all[j].p || !all[i].bytes || !all[j].bytes) continue;
+      if (overlaps(all[i].p, all[i].bytes, all[j].p, all[j].bytes))
+        return fail(AA_ERR_INVALID_ARG, std::string(fn) + ": " + all[i].name + " overlaps " + all[j].name);
     }
   return AA_OK;
 }
@@ -108,7 +111,7 @@ aa_status_t aa_layernorm_fwd(const void* X, const void* delta, const float* gamm
   if ((st = check_opt_ptr(mean, "mean", fn)) != AA_OK) return st;
   if ((st = check_opt_ptr(rstd, "rstd", fn)) != AA_OK) return st;
   const size_t n = size_t(M) * size_t(d), row = size_t(d) * 4;
-  const Range in[] = {{X, n * elem_size(x_dtype), S == X ? "S" : "X"},   // the sum may replace X in place
+  const Range in[] = {{X, n * elem_size(x_dtype), "X", S == X ? 4 : -1},   // the sum may replace X in place
                       {delta, n * elem_size(delta_dtype), "delta"},
                       {gamma, row, "gamma"},
                       {beta, row, "beta"},
@@ -116,7 +119,7 @@ aa_status_t aa_layernorm_fwd(const void* X, const void* delta, const float* gamm
                       {Y, n * elem_size(y_dtype), "Y"},
                       {mean, size_t(M) * 4, "mean"},
                       {rstd, size_t(M) * 4, "rstd"}};
-  if ((st = check_disjoint(in + 4, 4, in, 8, fn)) != AA_OK) return st;
+  if ((st = check_disjoint(in, 4, fn)) != AA_OK) return st;
   return aa::launch_norm_fwd({X, delta, gamma, beta, S, Y, mean, rstd, M, d, eps, x_dtype, delta_dtype, y_dtype},
                              stream);
 }
@@ -160,12 +163,12 @@ aa_status_t aa_layernorm_bwd(const void* X, const void* dY, const float* gamma, 
                       {gamma, row, "gamma"},
                       {mean, size_t(M) * 4, "mean"},
                       {rstd, size_t(M) * 4, "rstd"},
-                      {dS, n * elem_size(x_dtype), dS == dX ? "dX" : "dS"},   // dX may replace dS in place
+                      {dS, n * elem_size(x_dtype), "dS", dS == dX ? 6 : -1},   // dX may replace dS in place
                       {dX, n * elem_size(x_dtype), "dX"},
                       {dgamma, row, "dgamma"},
                       {dbeta, row, "dbeta"},
                       {workspace, need, "workspace"}};
-  if ((st = check_disjoint(in + 6, 4, in, 10, fn)) != AA_OK) return st;
+  if ((st = check_disjoint(in, 6, fn)) != AA_OK) return st;
   return aa::launch_norm_bwd({X, dY, gamma, mean, rstd, dS, dX, dgamma, dbeta, M, d, x_dtype, dy_dtype,
                               static_cast<float*>(workspace)},
                              stream);
@@ -202,7 +205,7 @@ aa_status_t aa_kv_append(const void* K, const void* V, int64_t ldk, int64_t ldv,
                       {pos, size_t(n) * 4, "pos"},
                       {k_pages, cache, "k_pages"},
                       {v_pages, cache, "v_pages"}};
-  if ((st = check_disjoint(in + 5, 2, in, 7, fn)) != AA_OK) return st;
+  if ((st = check_disjoint(in, 5, fn)) != AA_OK) return st;
   return aa::launch_kv_append({K, V, ldk, ldv, in_dtype, k_pages, v_pages, n_pages, page_size, n_kv_heads, head_dim,
                                page_table, n_seqs, max_pages, seq, pos, n},
                               stream);
@@ -263,7 +266,7 @@ aa_status_t aa_attn_decode(const void* Q, int64_t ldq, aa_dtype_t q_dtype, const
                       {lengths, size_t(n_seqs) * 4, "lengths"},
                       {O, size_t(n_seqs) * size_t(width) * elem_size(o_dtype), "O"},
                       {workspace, need, "workspace"}};
-  if ((st = check_disjoint(in + 5, 2, in, 7, fn)) != AA_OK) return st;
+  if ((st = check_disjoint(in, 5, fn)) != AA_OK) return st;
   return aa::launch_attn_decode({Q, ldq, q_dtype, k_pages, v_pages, n_pages, page_size, n_heads, n_kv_heads, head_dim,
                                  page_table, n_seqs, max_pages, lengths, scale, O, o_dtype, workspace},
                                 stream);
@@ -349,7 +352,7 @@ aa_status_t aa_moe_ffn_fwd(aa_plan_t up, aa_plan_t down, const void* X, const vo
                       {experts, pairs, "experts"},
                       {weights, pairs, "weights"},
                       {workspace, need, "workspace"}};
-  if ((st = check_disjoint(in + 6, 4, in, 10, fn)) != AA_OK) return st;
+  if ((st = check_disjoint(in, 6, fn)) != AA_OK) return st;
   return aa::launch_moe(*up, *down,
                         {X, Wr, n_experts, top_k, normalize, Wg_packed, Wu_packed, Wd_packed, Y, experts, weights, M,
                          pos_offset, row_types, workspace},

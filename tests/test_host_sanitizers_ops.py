@@ -26,3 +26,20 @@ def test_ops_host_code_under_asan_and_ubsan(tmp_path):
     r = subprocess.run([exe], capture_output=True, text=True, env=env, timeout=120)
     assert r.returncode == 0, (r.stdout[-2000:], r.stderr[-4000:])
     assert "host checks passed" in r.stdout
+
+
+def test_in_place_operands_do_not_hang_on_merged_literals(tmp_path):
+    """The same calls from a build in which equal string literals are objects of
+    their own (which the language leaves open): the in-place forms are accepted
+    all the same."""
+    if not os.path.exists(CLANG):
+        pytest.skip("clang++ of the ROCm toolchain not found")
+    flags = ["-std=c++17", "-O1", "-D__HIP_PLATFORM_AMD__", "-fwritable-strings", "-w",
+             "-I/opt/rocm/include", "-I" + os.path.join(ROOT, "include"), "-I" + CSRC]
+    srcs = [os.path.join(CSRC, "aa_plan.cpp"), os.path.join(CSRC, "aa_api_ops.cpp"),
+            os.path.join(HERE, "ops_stub_launch.cpp"), os.path.join(HERE, "in_place_driver.cpp")]
+    exe = str(tmp_path / "aa_ops_literals")
+    r = subprocess.run([CLANG, *flags, *srcs, "-o", exe, "-lpthread"], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-4000:]
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0 and "in-place calls passed" in r.stdout, (r.stdout, r.stderr)
