@@ -167,34 +167,35 @@ def prepare(case, seed):
         s["Y"] = torch.empty(n, D, dtype=DTYPES[c["y"]], device=DEV)
         s["experts"] = torch.empty(n, c["k"], dtype=torch.int32, device=DEV)
         s["weights"] = torch.empty(n, c["k"], device=DEV)
+    if own and c["op"] != "norm_fwd":
+        _workspace(s)
     return s
 
 
 # ------------------------------------------------------- the library's calls ---
 
 @functools.lru_cache(maxsize=None)
-def _scratch(bytes_):
-    return torch.empty(max(bytes_, 16), dtype=torch.uint8, device=DEV)
-
-
-@functools.lru_cache(maxsize=None)
-def _norm_bwd_scratch(M, d):
+def _moe_plans(law, q, D, F, y):
     import associative_algebra_block_amd as aa
-    return _scratch(aa.aa_layernorm_bwd_workspace(M, d))
+    return (aa.aa_plan_create(law, q, D, F, "pos_mod", 0, "bf16", "bf16"),
+            aa.aa_plan_create(law, q, F, D, "pos_mod", 0, "bf16", y))
 
 
-@functools.lru_cache(maxsize=None)
-def _attn_scratch(B, H, Hkv, D, page, most):
-    import associative_algebra_block_amd as aa
-    return _scratch(aa.aa_attn_decode_workspace(B, H, Hkv, D, page, most))
-
-
-@functools.lru_cache(maxsize=None)
-def _moe_plans(law, q, D, F, y, n, E, k):
-    import associative_algebra_block_amd as aa
-    up = aa.aa_plan_create(law, q, D, F, "pos_mod", 0, "bf16", "bf16")
-    down = aa.aa_plan_create(law, q, F, D, "pos_mod", 0, "bf16", y)
-    return up, down, _scratch(aa.aa_moe_ffn_workspace(up, down, E, k, n))
+def _workspace(s):
+    """The state's own workspace: calls that share one must not overlap in time,
+    and another state may be run on another stream."""
+    if "workspace" not in s:
+        import associative_algebra_block_amd as aa
+        n = 0
+        if s["op"] == "norm_bwd":
+            n = aa.aa_layernorm_bwd_workspace(s["M"], s["d"])
+        elif s["op"] == "attn":
+            n = aa.aa_attn_decode_workspace(s["B"], s["H"], s["Hkv"], s["D"], s["page"], s["most"])
+        elif s["op"] == "moe":
+            up, down = _moe_plans(s["law"], s["q"], s["D"], s["F"], s["y"])
+            n = aa.aa_moe_ffn_workspace(up, down, s["E"], s["k"], s["n"])
+        s["workspace"] = torch.empty(max(n, 16), dtype=torch.uint8, device=DEV)
+    return s["workspace"]
 
 
 def _run_own(s):
@@ -204,7 +205,7 @@ def _run_own(s):
         return [s["Y"], s["S"], s["mean"], s["rstd"]]
     if s["op"] == "norm_bwd":
         aa.aa_layernorm_bwd(s["X"], s["dY"], s["gamma"], s["mean"], s["rstd"], s["dX"], s["dgamma"], s["dbeta"],
-                            s["dS"], _norm_bwd_scratch(s["M"], s["d"]))
+                            s["dS"], _workspace(s))
         return [s["dX"], s["dgamma"], s["dbeta"]]
     if s["op"] == "attn":
         B, H, Hkv, D = s["B"], s["H"], s["Hkv"], s["D"]
@@ -212,12 +213,11 @@ def _run_own(s):
         K = s["qkv"][:, H * D : (H + Hkv) * D]
         V = s["qkv"][:, (H + Hkv) * D :]
         aa.aa_kv_append(K, V, s["Kp"], s["Vp"], s["table"], s["last"])
-        aa.aa_attn_decode(Q, s["Kp"], s["Vp"], s["table"], s["lens"], s["O"], D ** -0.5,
-                          _attn_scratch(B, H, Hkv, D, s["page"], s["most"]))
+        aa.aa_attn_decode(Q, s["Kp"], s["Vp"], s["table"], s["lens"], s["O"], D ** -0.5, _workspace(s))
         return [s["O"], s["Kp"], s["Vp"]]
-    up, down, ws = _moe_plans(s["law"], s["q"], s["D"], s["F"], s["y"], s["n"], s["E"], s["k"])
+    up, down = _moe_plans(s["law"], s["q"], s["D"], s["F"], s["y"])
     aa.aa_moe_ffn_fwd(up, down, s["X"], s["R"], s["Wg"], s["Wu"], s["Wd"], s["Y"], s["k"], s["norm"], s["experts"],
-                      s["weights"], ws, pos_offset=s["pos"])
+                      s["weights"], _workspace(s), pos_offset=s["pos"])
     return [s["Y"], s["experts"], s["weights"]]
 
 
