@@ -75,9 +75,9 @@ __global__ __launch_bounds__(256) void moe_router_kernel(MoeParams p) {
     const u32x4_t a = *reinterpret_cast<const u32x4_t*>(x + c);
     const u32x4_t b = *reinterpret_cast<const u32x4_t*>(w + c);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {   // a product of two bf16 that does not overflow is exact in float32
-      acc += double(lo_f(a[j]) * lo_f(b[j]));
-      acc += double(hi_f(a[j]) * hi_f(b[j]));
+    for (int j = 0; j < 4; ++j) {   // float64 holds every product of two bf16, float32 not the largest and smallest
+      acc = fma(double(lo_f(a[j])), double(lo_f(b[j])), acc);
+      acc = fma(double(hi_f(a[j])), double(hi_f(b[j])), acc);
     }
   }
 #pragma unroll

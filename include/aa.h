@@ -343,7 +343,7 @@ aa_status_t aa_attn_decode(const void* Q, int64_t ldq, aa_dtype_t q_dtype, const
  * and Wd_packed hold the experts' packed weights one after the other
  * (n_experts * D * F elements each).  Y is M x D of down's out_dtype; experts
  * and weights (M x top_k, in the order of the choice) may be NULL.  The logits
- * are summed in float64, everything else in float32; the hidden activation is
+ * are float64, products and sums, everything else float32; the hidden activation is
  * kept in float32 whatever up's out_dtype.  Rows whose explicit type lies
  * outside [0, q) are not written in any output.  A NaN logit is chosen first
  * and makes the token's weights NaN.  Limits: n_experts <= 512, top_k <= 64,

@@ -151,6 +151,32 @@ def test_explicit_types_and_rows_left_alone():
     L.check(X[kept], 3, True, types[kept].cpu().numpy(), Y[kept], experts[kept], weights[kept])
 
 
+@pytest.mark.parametrize("law,q,E,k", [("Qq", 2, 8, 3), ("Q2xQ2", 4, 70, 5)])
+@pytest.mark.parametrize("x_exp,r_exp", [(-80, -60), (-63, -66), (80, 60), (64, 63), (-100, -50)])
+def test_choice_where_float32_has_no_such_products(law, q, E, k, x_exp, r_exp):
+    """Logits are float64: scaling the token and the router by powers of two
+    scales them exactly, also where a float32 product would be infinite, zero or
+    short of digits.  (The experts' own float32 sums need not hold such values;
+    weights are those of the logits' differences.)"""
+    say("moe choice", law, q, E, k, x_exp, r_exp)
+    L = Layer(law, q, 64, 64, E, 37)
+    X = inp.gaussian((6, 64), 5, 1.0, BF16, DEV)
+    base = (X.double() @ L.R.double().t()).cpu().numpy()
+    X = (X.double() * 2.0 ** x_exp).to(BF16)
+    L.R = (L.R.double() * 2.0 ** r_exp).to(BF16)
+    assert torch.equal((X.double() @ L.R.double().t()).cpu(), torch.from_numpy(base * 2.0 ** (x_exp + r_exp)))
+    for norm in (True, False):
+        _, experts, weights = L.run(X, k, norm)
+        r = base * 2.0 ** (x_exp + r_exp)
+        for t in range(6):
+            sel = sorted(range(E), key=lambda e: (-r[t, e], e))[:k]
+            assert experts[t].tolist() == sel, (t, experts[t].tolist(), sel)
+            ex = np.exp(r[t] - r[t].max())
+            w = ex[sel] / (ex[sel].sum() if norm else ex.sum())
+            # a weight below float32's normal values is off by half its smallest step
+            assert np.all(np.abs(weights[t].double().cpu().numpy() - w) <= (E + 24) * U * w + 2.0 ** -150)
+
+
 def test_a_token_of_nan_stays_alone():
     L = Layer("Qq", 2, 64, 64, 8, 17)
     X = inp.gaussian((5, 64), 5, 1.0, BF16, DEV)
