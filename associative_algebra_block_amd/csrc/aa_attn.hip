@@ -110,9 +110,12 @@ template <bool B> struct Bool {
   static constexpr bool value = B;
 };
 
-// x = hi + mid + lo exactly to 24 bits, each a bf16.
-__device__ inline void split3(float x, __bf16* t) {
-  t[0] = (__bf16)x;
+// x = hi + mid + lo exactly to 24 bits, each a bf16.  lead is x, or x held within
+// bf16's range: bf16 rounds the largest float32 values up to infinity, and the
+// largest bf16 leaves 16 digits of them as a rounding does.
+constexpr float kMaxBf16 = 0x1.fep127f;
+__device__ inline void split3(float x, float lead, __bf16* t) {
+  t[0] = (__bf16)lead;
   float r = x - float(t[0]);
   t[1] = (__bf16)r;
   t[2] = (__bf16)(r - float(t[1]));
@@ -178,7 +181,9 @@ __global__ __launch_bounds__(kAttnWaves * 64, DC <= 5 ? 2 : 1) void attn_decode_
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         __bf16 t[3];
-        split3(raw[c][e], t);
+        // an infinite or NaN query gives NaN with any keys, here by its lower terms
+        const float x = raw[c][e];
+        split3(x, NQ > 1 ? __builtin_amdgcn_fmed3f(x, -kMaxBf16, kMaxBf16) : x, t);
 #pragma unroll
         for (int k = 0; k < NQ; ++k) q[k][c][e] = t[k];
       }
@@ -340,7 +345,7 @@ __global__ __launch_bounds__(kAttnWaves * 64, DC <= 5 ? 2 : 1) void attn_decode_
         const float e = __builtin_amdgcn_exp2f(s[t][i] - mu);
         sum += e;
         __bf16 term[3];
-        split3(e, term);
+        split3(e, e, term);
 #pragma unroll
         for (int k = 0; k < NP; ++k) pf[k][4 * t + i] = term[k];
       }

@@ -185,6 +185,30 @@ def test_infinities_and_nan_follow_the_formula():
     check(c, Q, O, 0.3, 2)
 
 
+@pytest.mark.parametrize("ot", [F32, BF16])
+@pytest.mark.parametrize("D", [8, 40, 160])
+def test_queries_beyond_the_largest_bf16_value(D, ot):
+    """float32 queries up to float32's largest value, which a rounding to bf16
+    would make infinite, against keys so small that the scores are of order
+    one; infinite and NaN queries give NaN."""
+    top = torch.finfo(F32).max
+    c = Cache([70, 700, 5, 9], 1, D, 16, 50 + D)
+    for k in c.k:                                             # no denormal values
+        k.copy_((torch.sign(k.float()) * (1 + k.float().abs().remainder(1)) * 2.0 ** -124).to(BF16))
+    c.write()
+    Q = torch.zeros(4, 2, D)
+    Q[0, 0, 3], Q[0, 1, 2] = top, -top
+    Q[1, 0, 0], Q[1, 0, 7], Q[1, 1, 5] = -top, top * (1 - 2.0 ** -9), top * (1 - 2.0 ** -10)
+    Q[2, 0, 4], Q[2, 1, 4] = torch.finfo(BF16).max, top * 0.5
+    Q[3, 0, 1], Q[3, 1, 1] = float("inf"), float("nan")
+    Q = Q.to(DEV)
+    O = attend(c, Q, ot, 0.05, 2)
+    assert bool(O[3].isnan().all())
+    c.k[3], c.v[3] = c.k[3][:0], c.v[3][:0]
+    O[3] = 0
+    check(c, Q, O, 0.05, 2)
+
+
 def test_infinite_feature_beside_a_padded_chunk():
     """Head dim 40: the second 32-wide chunk of features is padded; an infinite
     last feature must not meet the padding."""
