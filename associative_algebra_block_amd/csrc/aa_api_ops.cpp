@@ -244,7 +244,8 @@ aa_status_t aa_attn_decode(const void* Q, int64_t ldq, aa_dtype_t q_dtype, const
   if ((st = check_dtype(o_dtype, "o_dtype", fn)) != AA_OK) return st;
   if ((st = check_cache(n_pages, page_size, n_kv_heads, head_dim, n_seqs, max_pages, fn)) != AA_OK) return st;
   if ((st = check_heads(n_seqs, n_heads, n_kv_heads, fn)) != AA_OK) return st;
-  if (!isfinite(scale)) return fail(AA_ERR_INVALID_ARG, "aa_attn_decode: scale is not finite");
+  // the kernel takes scores to base 2, whose factor must be finite too
+  if (!(fabsf(scale) <= 0x1p127f)) return fail(AA_ERR_INVALID_ARG, "aa_attn_decode: scale is not finite or beyond 2^127");
   const int64_t width = int64_t(n_heads) * head_dim;
   if ((st = check_ld(ldq, width, "ldq", fn)) != AA_OK) return st;
   if (n_seqs == 0) return AA_OK;

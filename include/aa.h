@@ -315,11 +315,11 @@ aa_status_t aa_kv_append(const void* K, const void* V, int64_t ldk, int64_t ldv,
  * 0 gets zeros; one whose length is negative or beyond its table, or that
  * needs a page outside [0, n_pages), gets NaN, and nothing outside the cache
  * is read.  Slots behind a sequence's end may hold anything; an infinite value
- * before it makes its feature's output infinite or NaN.  Scores, softmax
- * statistics and sums are float32; neither queries nor probabilities are
- * rounded to bf16.  Workspace: at least what aa_attn_decode_workspace reports;
- * its contents are overwritten, and calls that share one must not overlap in
- * time.  n_seqs == 0 is a no-op. */
+ * before it makes its feature's output infinite or NaN.  scale is finite, at most
+ * 2^127 in magnitude.  Scores, softmax statistics and sums are float32; neither
+ * queries nor probabilities are rounded to bf16.  Workspace: at least what
+ * aa_attn_decode_workspace reports; its contents are overwritten, and calls that
+ * share one must not overlap in time.  n_seqs == 0 is a no-op. */
 aa_status_t aa_attn_decode_workspace(int64_t n_seqs, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
                                      int32_t page_size, int64_t max_pages, size_t* bytes);
 aa_status_t aa_attn_decode(const void* Q, int64_t ldq, aa_dtype_t q_dtype, const void* k_pages, const void* v_pages,
@@ -343,9 +343,9 @@ aa_status_t aa_attn_decode(const void* Q, int64_t ldq, aa_dtype_t q_dtype, const
  * and Wd_packed hold the experts' packed weights one after the other
  * (n_experts * D * F elements each).  Y is M x D of down's out_dtype; experts
  * and weights (M x top_k, in the order of the choice) may be NULL.  The logits
- * are float64, products and sums, everything else float32; the hidden activation is
- * kept in float32 whatever up's out_dtype.  Rows whose explicit type lies
- * outside [0, q) are not written in any output.  A NaN logit is chosen first
+ * are float64, products and sums, everything else float32; the hidden
+ * activation is kept in float32 whatever up's out_dtype.  Rows whose explicit
+ * type lies outside [0, q) are not written in any output.  A NaN logit is chosen first
  * and makes the token's weights NaN.  Limits: n_experts <= 512, top_k <= 64,
  * M * top_k <= 65535, D and F below 2^24; every (token, expert) pair reads its
  * weights for itself, so many tokens are better served expert by expert with

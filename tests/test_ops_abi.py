@@ -107,6 +107,14 @@ def test_attn_decode(lib, status, changed):
     assert call(lib, "aa_attn_decode", ATTN, **changed) == status
 
 
+@pytest.mark.parametrize("scale", [1.8e38, -1.8e38, 3.4e38])
+def test_attn_scales_beyond_the_kernels_base(lib, scale):
+    """Scores are taken to base 2: a scale whose product with log2 e is infinite
+    is refused."""
+    assert call(lib, "aa_attn_decode", ATTN, scale=scale) == BAD
+    assert call(lib, "aa_attn_decode", ATTN, scale=scale / 2, n_seqs=0) == OK
+
+
 def test_attn_workspace(lib):
     n = ctypes.c_size_t(0)
     f = lib.aa_attn_decode_workspace
