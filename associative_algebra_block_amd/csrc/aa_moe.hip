@@ -28,6 +28,7 @@
 
 #include "aa_device.h"
 #include "aa_internal.h"
+#include "aa_rules.h"
 
 namespace aa {
 namespace {
@@ -195,7 +196,7 @@ __device__ inline float quad_sum(float v) {   // over the four lanes of a column
 // zeros behind the last.  By the keys' upper halves alone (exact == false)
 // experts that agree in them get the same place, which the caller sees: two such
 // logits differ by less than 2^-20 of themselves.
-constexpr int kUpWaves = 8, kUpThreads = 64 * kUpWaves;
+constexpr int kUpWaves = kMoeUpWaves, kUpThreads = 64 * kUpWaves;
 static_assert(kUpThreads >= kMoeMaxExperts, "a thread for every expert");
 template <bool exact>
 __device__ inline int place_of(const uint64_t* keys, const uint32_t* upper, int E, int e, int per) {
@@ -441,48 +442,24 @@ aa_status_t launch_moe(const aa_plan_s& up, const aa_plan_s& down, const MoeCall
   launch(moe_router_kernel, dim3((p.E + 3) / 4, M), dim3(256), 0u, stream, p);
   aa_status_t st = after_launch(stream, "moe_router_kernel");
   if (st != AA_OK) return st;
-  const uint32_t strips = uint32_t(p.F / 16);
+  const MoeRule rule = moe_rule(up.law == AA_LAW_Q2XQ2, p.q, p.D, p.F, p.top_k, c.M);
   const dim3 block(kUpThreads);
-  // Waves a strip: as many as repay their join.  Measured (us of the whole call)
-  // with 1, 2, 4 and 8, for sums of 8 steps of 32 rows (q = 16, 2048 -> 768) at 384
-  // strips 14.0, 13.2, 12.8, 14.1; at 768 15.5, 14.9, 15.5, 16.7; at 1536 17.2, 17.8,
-  // 17.9, 23.0.  For 16 and more steps (Q2 x Q2, 768 -> 2048) at 256 strips 19.1,
-  // 16.0, 14.8, 13.9; at 1280 20.6, 19.7, 18.8, 20.8; at 5120 44.3, 41.7, 47.6, 59.4;
-  // at 10240 48.3, 53.0, 64.8, 90.1.
-  const int groups = up.law == AA_LAW_Q2XQ2 ? 4 : std::min(int(up.q), 2);
-  const bool long_sums = groups * (up.d_in / up.q) >= 16 * 32;
-  const uint64_t all_strips = uint64_t(pairs) * strips;
-  const int ws_up = long_sums && all_strips <= 256 ? 8 : all_strips <= (long_sums ? 1536 : 512) ? 4
-                    : all_strips <= (long_sums ? 8192 : 1024) ? 2 : 1;
-  p.parts = (strips * ws_up + kUpWaves - 1) / kUpWaves;
+  p.parts = rule.up_parts;
   p.pairs = pairs;
-  const dim3 grid = p.parts % 8 && pairs >= 16 ? dim3(8 * p.parts, (pairs + 7) / 8) : dim3(p.parts, pairs);
-  if (ws_up == 8) launch((moe_up_kernel<8>), grid, block, 0u, stream, p);
-  else if (ws_up == 4) launch((moe_up_kernel<4>), grid, block, 0u, stream, p);
-  else if (ws_up == 2) launch((moe_up_kernel<2>), grid, block, 0u, stream, p);
+  const dim3 grid = rule.rows_of_eight ? dim3(8 * p.parts, (pairs + 7) / 8) : dim3(p.parts, pairs);
+  if (rule.up_waves == 8) launch((moe_up_kernel<8>), grid, block, 0u, stream, p);
+  else if (rule.up_waves == 4) launch((moe_up_kernel<4>), grid, block, 0u, stream, p);
+  else if (rule.up_waves == 2) launch((moe_up_kernel<2>), grid, block, 0u, stream, p);
   else launch((moe_up_kernel<1>), grid, block, 0u, stream, p);
   st = after_launch(stream, "moe_up_kernel");
   if (st != AA_OK) return st;
   const uint32_t out_strips = uint32_t(p.D / 16), q = uint32_t(p.q);
-  // Two strips a workgroup, which share the hidden activation's loads, where there
-  // are enough of them, else one, with four or, for long sums, sixteen waves:
-  // (2 strips x 8 waves, 1 x 4, 1 x 16) take for 1, 5, 10 and 20 tokens of Q2 x Q2
-  // experts (48, 240, 480, 960 strips, 128 steps) 15.9, 16.2, 14.3; 20.9, 20.7, 18.7;
-  // 24.9, 26.7, 27.2; 33.2, 35.9, 42.1 us; for 2 and 16 tokens of q = 16, 2048 -> 768
-  // (256, 2048 strips, 32 steps) 14.8, 14.6, 16.2 and 32.1, 33.5, 60.5.  Short sums
-  // of very many strips do with four waves: 32 tokens (4096 strips) 51.9 and 53.0.
-  // Workgroups of 16 waves are one a unit, so more than 256 of them take two turns:
-  // q = 2, 640 -> 1440, 7 tokens (280 strips, 276 steps) 42 us, 2 x 8 37.
-  const int steps = p.top_k * groups * int((p.F / p.q + 31) / 32);
-  const uint64_t all_out = uint64_t(M) * out_strips;
-  if (all_out >= 1536 && steps <= 64)
-    launch((moe_down_kernel<2, 4>), dim3((out_strips / q + 1) / 2 * q, M), dim3(256), 0u, stream, p);
-  else if (all_out >= 400 || (steps > 64 && all_out > 256))
-    launch((moe_down_kernel<2, 8>), dim3((out_strips / q + 1) / 2 * q, M), dim3(512), 0u, stream, p);
-  else if (steps <= 64)
-    launch((moe_down_kernel<1, 4>), dim3(out_strips, M), dim3(256), 0u, stream, p);
-  else
-    launch((moe_down_kernel<1, 16>), dim3(out_strips, M), dim3(1024), 0u, stream, p);
+  const dim3 down_grid((out_strips / q + rule.down_strips - 1) / rule.down_strips * q, M);
+  const dim3 down_block(64 * rule.down_waves);
+  if (rule.down_strips == 2 && rule.down_waves == 4) launch((moe_down_kernel<2, 4>), down_grid, down_block, 0u, stream, p);
+  else if (rule.down_strips == 2) launch((moe_down_kernel<2, 8>), down_grid, down_block, 0u, stream, p);
+  else if (rule.down_waves == 4) launch((moe_down_kernel<1, 4>), down_grid, down_block, 0u, stream, p);
+  else launch((moe_down_kernel<1, 16>), down_grid, down_block, 0u, stream, p);
   return after_launch(stream, "moe_down_kernel");
 }
 

@@ -22,4 +22,47 @@ inline bool append_turns(int64_t n, int head_dim) {
   return n >= 8 * int64_t(head_dim) && append_turn_workgroups(n) * kTurnThreads <= kMaxGridThreads;
 }
 
+// The kernels of a mixture-of-experts call: waves per 16-column strip of gate and
+// up (kMoeUpWaves a workgroup, up_parts workgroups a pair, pairs in rows of eight
+// or one a row), and strips and waves a workgroup of the down projection.
+constexpr int kMoeUpWaves = 8;
+struct MoeRule {
+  int up_waves;
+  uint32_t up_parts;
+  bool rows_of_eight;
+  int down_strips, down_waves;
+};
+inline MoeRule moe_rule(bool q2xq2, int q, int64_t D, int64_t F, int top_k, int64_t M) {
+  MoeRule r;
+  const uint64_t pairs = uint64_t(M) * uint64_t(top_k), strips = uint64_t(F / 16);
+  const int groups = q2xq2 ? 4 : q < 2 ? q : 2;   // of a leaf, at most
+  // Waves a strip: as many as repay their join.  Measured (us of the whole call)
+  // with 1, 2, 4 and 8, for sums of 8 steps of 32 rows (q = 16, 2048 -> 768) at 384
+  // strips 14.0, 13.2, 12.8, 14.1; at 768 15.5, 14.9, 15.5, 16.7; at 1536 17.2, 17.8,
+  // 17.9, 23.0.  For 16 and more steps (Q2 x Q2, 768 -> 2048) at 256 strips 19.1,
+  // 16.0, 14.8, 13.9; at 1280 20.6, 19.7, 18.8, 20.8; at 5120 44.3, 41.7, 47.6, 59.4;
+  // at 10240 48.3, 53.0, 64.8, 90.1.
+  const bool long_sums = groups * (D / q) >= 16 * 32;
+  const uint64_t all_strips = pairs * strips;
+  r.up_waves = long_sums && all_strips <= 256 ? 8 : all_strips <= (long_sums ? 1536 : 512) ? 4
+               : all_strips <= (long_sums ? 8192 : 1024) ? 2 : 1;
+  r.up_parts = uint32_t((strips * r.up_waves + kMoeUpWaves - 1) / kMoeUpWaves);
+  r.rows_of_eight = r.up_parts % 8 && pairs >= 16;
+  // Two strips a workgroup, which share the hidden activation's loads, where there
+  // are enough of them, else one, with four or, for long sums, sixteen waves:
+  // (2 strips x 8 waves, 1 x 4, 1 x 16) take for 1, 5, 10 and 20 tokens of Q2 x Q2
+  // experts (48, 240, 480, 960 strips, 128 steps) 15.9, 16.2, 14.3; 20.9, 20.7, 18.7;
+  // 24.9, 26.7, 27.2; 33.2, 35.9, 42.1 us; for 2 and 16 tokens of q = 16, 2048 -> 768
+  // (256, 2048 strips, 32 steps) 14.8, 14.6, 16.2 and 32.1, 33.5, 60.5.  Short sums
+  // of very many strips do with four waves: 32 tokens (4096 strips) 51.9 and 53.0.
+  // Workgroups of 16 waves are one a unit, so more than 256 of them take two turns:
+  // q = 2, 640 -> 1440, 7 tokens (280 strips, 276 steps) 42 us, 2 x 8 37.
+  const int64_t steps = top_k * int64_t(groups) * ((F / q + 31) / 32);
+  const uint64_t all_out = uint64_t(M) * uint64_t(D / 16);
+  if (all_out >= 1536 && steps <= 64) r.down_strips = 2, r.down_waves = 4;
+  else if (all_out >= 400 || (steps > 64 && all_out > 256)) r.down_strips = 2, r.down_waves = 8;
+  else r.down_strips = 1, r.down_waves = steps <= 64 ? 4 : 16;
+  return r;
+}
+
 }  // namespace aa

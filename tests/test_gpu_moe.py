@@ -115,6 +115,29 @@ def test_layer(law, q, D, F, E, k, M, norm, out, pos):
     L.check(X, k, norm, oracle.types_pos_mod(M, q, pos), Y, experts, weights)
 
 
+# the kernels that the sizes above do not reach: long sums of few strips (eight waves a strip), two strips a
+# workgroup of eight waves, and of either width with a strip left over (an odd number of them in an output group)
+KERNEL_CASES = [
+    ("Q2xQ2", 4, 768, 1536, 8, 2, 1, True, "f32", 3),
+    ("Q2xQ2", 4, 768, 1536, 8, 2, 1, False, "bf16", 6),
+    ("Q2xQ2", 4, 768, 1536, 8, 2, 20, True, "f32", 1),
+    ("Q2xQ2", 4, 768, 1536, 8, 2, 20, False, "bf16", 2),
+    ("Qq", 2, 640, 1440, 15, 6, 7, True, "f32", 0),
+    ("Qq", 4, 192, 64, 5, 2, 34, True, "f32", 3),
+    ("Qq", 4, 192, 64, 5, 3, 35, False, "bf16", 1),
+    ("Qq", 4, 192, 64, 5, 2, 130, True, "f32", 2),
+    ("Qq", 4, 192, 64, 5, 2, 131, False, "bf16", 0),
+    ("Qq", 1, 80, 48, 4, 2, 90, True, "f32", 0),
+    ("Qq", 4, 128, 64, 4, 2, 400, False, "bf16", 2),
+    ("Qq", 4, 128, 64, 4, 2, 400, True, "f32", 2),
+]
+
+
+@pytest.mark.parametrize("law,q,D,F,E,k,M,norm,out,pos", KERNEL_CASES)
+def test_layer_on_every_kernel(law, q, D, F, E, k, M, norm, out, pos):
+    test_layer(law, q, D, F, E, k, M, norm, out, pos)
+
+
 def test_equal_logits_go_to_the_lower_index():
     L = Layer("Qq", 2, 64, 64, 70, 3)
     L.R[5], L.R[69], L.R[64] = L.R[33], L.R[33], L.R[33]
