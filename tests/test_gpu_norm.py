@@ -145,6 +145,26 @@ def test_backward(M, d, xt, dyt, ds):
     assert untouched(xbuf) and untouched(gbuf) and untouched(bbuf)
 
 
+@pytest.mark.parametrize("M,d", [(1, 768), (3, 5), (5, 1025), (257, 2049), (1003, 2047), (2300, 8192), (600, 16383),
+                                 (4600, 2048), (9000, 1030), (12288, 768), (12289, 1024), (20001, 300), (65537, 64)])
+@pytest.mark.parametrize("xt,dyt", [(F32, F32), (BF16, BF16), (F32, BF16), (BF16, F32)])
+def test_every_row_counts_once_in_the_weights_gradients(M, d, xt, dyt):
+    """Small whole numbers with mean 0 and rstd 1: xh is X, every product and sum
+    is a whole number below 2^24 (9 M at most), so the sums are exact in any
+    order and a row lost or taken twice shows in every column that it touches."""
+    assert 9 * M < 1 << 24
+    say("norm bwd exact", M, d, xt, dyt)
+    g = torch.Generator().manual_seed(M + d)
+    X, dY = (torch.randint(-3, 4, (M, d), generator=g) for _ in range(2))
+    dY += (dY == 0) * 2                                      # no row is silent
+    mean, rstd = torch.zeros(M, device=DEV), torch.ones(M, device=DEV)
+    dX = torch.empty(M, d, dtype=xt, device=DEV)
+    dG, dB = torch.empty(d, device=DEV), torch.empty(d, device=DEV)
+    ws = torch.full((aa.aa_layernorm_bwd_workspace(M, d),), 255, dtype=torch.uint8, device=DEV)
+    aa.aa_layernorm_bwd(X.to(xt).to(DEV), dY.to(dyt).to(DEV), None, mean, rstd, dX, dG, dB, None, ws)
+    assert torch.equal(dG.cpu().long(), (X * dY).sum(0)) and torch.equal(dB.cpu().long(), dY.sum(0))
+
+
 def test_gradient_formula_against_differences():
     """The formula that the tests above hold the kernel to, against central
     differences of the forward definition in float64 (step 1e-5: truncation
