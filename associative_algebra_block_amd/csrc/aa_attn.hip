@@ -14,8 +14,8 @@
 // lane that needs it for the second product: lane (head n, group g) gets keys
 // 8 g + 4 t + i in element i of fragment t, and feeds keys 8 g .. 8 g + 7.
 //
-// The cache crosses HBM once and that bounds the call: 4 G operations a loaded
-// byte pair (G query heads share a kv head) are far below the matrix rate even
+// The cache crosses HBM once and that bounds the call: 2 G operations a loaded
+// value (G query heads share a kv head) are far below the matrix rate even
 // where only one of a fragment's 16 head columns is in use.  The matrix slack
 // pays for exactness: float32 queries go in as three bf16 terms, the
 // probabilities as two (three for float32 outputs), so neither is rounded to
@@ -221,9 +221,14 @@ __global__ __launch_bounds__(kAttnWaves * 64, DC <= 5 ? 2 : 1) void attn_decode_
   // Memory straight to the wave's own LDS, 1 KiB in a row for each load: slot
   // 64 i + lane of load i takes one piece of 16 bytes (slots behind the last
   // piece take that one again).  The keys' whole lines are fetched past the
-  // caches (nontemporal): they are used once.  So are the values' from pages of
-  // up to 32 positions; from larger ones a feature's 64 bytes are half a line,
-  // whose other half a neighbour wave wants.
+  // caches (nontemporal), as a long or large cache is read but once: the ragged
+  // batch of the head comment takes 108 us with its append and join, with keys
+  // through the caches 113.5, the long sequence 98 and 106.  Where tiles of heads
+  // or sequences read the same keys, and where the whole cache is small, it costs
+  // a little: 8 sequences of 8000 with 40 heads on one kv head 31.5 us against
+  // 29.5, 16 of 8000 on the same pages 46.4 and 44.5.  The values are fetched past
+  // the caches from pages of up to 32 positions; from larger ones a feature's 64
+  // bytes are half a line, whose other half a neighbour wave wants.
   const int R = p.D / 8;              // pieces of a key
   const bool small = p.page_shift == 4;
   unsigned char* kmine = s_stage + wave * kStage;
@@ -621,6 +626,12 @@ void launch_attn_dc(const AttnParams& p, bool q_f32, uint32_t grid, hipStream_t 
 // 1000 to 8192 in 4 and 8 parts 102.8 and 100.3; one of 2000 in parts of at least
 // 4 and 8 steps 9.3 and 11.0.  32 heads of 24, eight sequences of up to 1500 in
 // 1, 2, 4, 8 parts: 13.8, 14.5, 13.7, 13.4; four: 13.8, 11.9, 10.4, 10.4.
+// All of these fill their tables.  In a wider table a part is at least the
+// table's steps over its parts (min_tiles), so short sequences get few of them:
+// one sequence of 2000 takes 9.4 us in a table of 2048 positions and 18.6 in one
+// of 32768, one of 8192 14.7 and 19.6, four of 2000 13.8 and 19.7; with 32 heads
+// of 24, one of 200 takes 4.9 us in a table of 256 and 7.7, with a join, in one of
+// 1536.
 int attn_nsplit(int64_t n_seqs, int H, int Hkv, int D, int64_t max_pages, int page) {
   const int64_t rows = std::max<int64_t>(n_seqs * Hkv * head_tiles_of(H / Hkv), 1);
   const int64_t tiles = (max_pages * page + kKeys - 1) / kKeys;

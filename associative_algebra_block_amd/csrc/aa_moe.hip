@@ -10,11 +10,12 @@
 // call is reading those blocks (9.1 MB for one token of the 2048 -> 768
 // experts at q = 16 with 8 chosen) at a latency that few tokens do not hide,
 // so every kernel spreads its loads over as many waves as there are 16-column
-// strips and issues them before the first use.  One token takes 4.0 + 6.0 + 4.0
+// strips and issues them before the first use.  One token takes 3.0 + 5.8 + 4.0
 // us (logits, gate and up, down), each within a few us of an empty launch;
-// sixteen, 120 MB, 4.7 + 18.3 + 11.4 us: 4 TB/s over the last two, where a plain
-// read of as much reaches 6.8; the choice in front of the loads and the tails
-// take the rest.
+// sixteen, 120 MB, 4.6 + 17.8 + 11.6 us: 4 TB/s over the last two, where a plain
+// read of as much reaches 6.8.  The choice in front of gate and up's loads, the
+// tails and the down projection's half slabs (every second step of its 48-row
+// blocks fetches 512 bytes instead of 1024) take the rest.
 //
 // Three launches: the logits; gate and up of every (token, expert) pair; the
 // down projection with the weighted sum.  The choice itself is no launch: each
@@ -119,7 +120,7 @@ __device__ inline Groups leaf_groups_of(int law, int i, int k) {
 // back a step at a time: done by the scalar unit the addresses took longer than
 // the loads.  U steps' loads go out without a branch or a use between them (8,
 // or 4 with two matrices: at 8 those take 115 registers and fewer waves fit,
-// 22.7 against 19.3 us for 16 tokens); a step behind the end loads the last
+// 36.1 against 33.3 us for a call of 16 tokens); a step behind the end loads the last
 // one's data again and is left out of the sum, as are the lanes behind the half
 // slab that ends a block of an odd multiple of 16 rows.
 template <int NM, typename TX, typename FAt, typename FShare>
@@ -233,8 +234,8 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(MoeParams p) {
   // turn: where a pair has a multiple of eight, those of a strip lie on one die,
   // and pairs that share an expert meet there.  Where it has not, a row of the
   // grid is eight pairs, and each die takes all workgroups of an eighth of the
-  // parts (q = 2, 2048 -> 768, 16 tokens: 56 against 61 us; 640 -> 1440, 7 tokens,
-  // 42 pairs: 35 against 37; with 16 parts, where both do it, 83 against 77).
+  // parts (q = 2, 2048 -> 768, 16 tokens: 55 against 61 us; 640 -> 1440, 7 tokens,
+  // 42 pairs: 35 against 37; with 16 parts, where both do it, 82 against 78).
   uint32_t part = blockIdx.x, pair = blockIdx.y;
   if (gridDim.x != p.parts) {
     const uint32_t place = blockIdx.x % 8 * p.parts + blockIdx.x / 8;
@@ -283,7 +284,7 @@ __global__ __launch_bounds__(kUpThreads) void moe_up_kernel(MoeParams p) {
   // This pair's weight, for the next kernel and the caller.  In a workgroup of its
   // own it takes 0.3 us less for one token, but with one workgroup more a pair
   // those that read the same strip of an expert no longer fall on the same die
-  // (80 tokens of Q2 x Q2 experts: 106 instead of 77 us).
+  // (80 tokens of 8 Q2 x Q2 experts, 768 -> 2048, 2 chosen: 106 instead of 77 us).
   if (part == 0) {
     const uint64_t top_key = s_top;
     const double top = top_key == ~uint64_t(0) ? double(NAN)

@@ -13,8 +13,10 @@
 // variance are two passes over registers (the variance is that of the
 // deviations, so a large common offset costs no digits), and every tensor
 // crosses HBM once.  All sums are float32.  12288 rows of 768 with a residual
-// operand (132 MB) take 20.8 us forward and 25.3 + 5.2 us backward, where a copy
-// of as many bytes takes 27; one row takes 2.8 us, which a launch costs anyhow.
+// operand (132 MB) take 21 us forward and 29.4 us backward (its kernels traced
+// alone 25.5 and 5.2), where a copy of as many bytes takes 27; one row takes 2.8
+// us, which a launch costs anyhow.  Times below are of whole calls that follow one
+// another, backward ones with both weights' gradients.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -346,8 +348,8 @@ __global__ __launch_bounds__(1024) void norm_bwd_reduce_kernel(const float* part
 
 // Rows are dealt to at most 16 workgroups a compute unit.  With half as many,
 // which still fill it, the rows of a wave follow one another and the second
-// one's loads wait for the first one's stores: 30.5 against 27.9 us for 12288
-// rows of 768.
+// one's loads wait for the first one's stores: 22.2 against 21.1 us for 12288
+// rows of 768; with twice as many 21.1.
 int64_t fwd_grid(int64_t M, int wpr) {
   const int64_t rows_per_wg = wpr == 1 ? 4 : 1;
   const int64_t wgs = (M + rows_per_wg - 1) / rows_per_wg;
@@ -358,22 +360,22 @@ int64_t fwd_grid(int64_t M, int wpr) {
 
 // Outputs that no L2 can hold until the next kernel reads them (the eight of
 // 4 MB together) are stored past the caches: 12288 rows of 768 take 21.0 against
-// 27.9 us forward and 26.6 against 29.6 us backward, and followed by the FFN and
-// the next norm as long as without (131.5 and 132.5 us).  Smaller ones stay for
-// the next kernel: norm, FFN and norm of 2048 rows of 2048 took 42 us with them
-// cached and 45.5 us without.
+// 27.9 us forward and 29.5 against 32.8 us backward; norm, FFN (Q2 x Q2, 1536
+// wide) and norm take 108.0 and 107.4.  Smaller ones are left where the next
+// kernel may find them: norm, FFN (q = 16, 768 wide) and norm of 2048 rows of 2048
+// take 36.0 us past the caches and 36.5 through them, of 4096 rows 63.6 and 62.9.
 constexpr int64_t kL2Bytes = int64_t(32) << 20;
 int32_t past_caches(int64_t values, int64_t bytes_each) { return values * bytes_each > kL2Bytes ? 1 : 0; }
 int64_t size_of(aa_dtype_t t) { return t == AA_F32 ? 4 : 2; }
 
 // Workgroups of the backward kernel, each of which writes 2 d partial sums.
-// One wave a row: 512 (12288 float32 rows of 768 with dS take 33.6, 29.7 and
-// 31.2 us with 256, 512 and 1024).  Wider rows: at least eight a workgroup from
-// 256 on (1000 rows of 2048 take 14.1 us with 256 and 17.2 with 512, whose sums
+// One wave a row: 512 (12288 float32 rows of 768 with dS take 34.0, 29.4 and
+// 31.3 us with 256, 512 and 1024).  Wider rows: at least eight a workgroup from
+// 256 on (1000 rows of 2048 take 14.2 us with 256 and 17.2 with 512, whose sums
 // take longer to write and join than the rows), and not so many that the rows in
-// flight, 4 MB, outgrow the L2s: 4600 float32 rows of 2048 take 29.4, 23.5 and
-// 24.8 us with 256, 512 and 1024; 8000 bf16 rows 49.4, 43.3 and 40.1; 10000 rows
-// of 4096 with 256 and 512: 76 and 85 in float32, 77 and 63 in bf16.
+// flight, 4 MB, outgrow the L2s: 4600 float32 rows of 2048 take 29.8, 23.5 and
+// 24.7 us with 256, 512 and 1024; 8000 bf16 rows 48.0, 37.8 and 33.4; 10000 rows
+// of 4096 with 256 and 512: 76 and 85 in float32, 76 and 64 in bf16.
 int64_t bwd_grid(int64_t M, int64_t d, int64_t size) {
   const bool narrow = d <= 1024;
   const int64_t wgs = narrow ? (M + kBwdWaves - 1) / kBwdWaves : M;
@@ -384,18 +386,19 @@ int64_t bwd_grid(int64_t M, int64_t d, int64_t size) {
 }
 
 // Calls CALL(waves per row, chunks) for a row of d features.  Up to 1024 one
-// wave a row, no barrier: 12288 float32 rows of 768 take 19.3 us forward and 31.7
-// backward, with four waves 21.3 and 33.3 (64 rows: 3.6 and 3.3 forward).
-// Beyond, 8 to 32 features a lane:
-//   2048 (4608 float32 rows)  4 x 8 features 19.6, 8 x 4 21.6, 1 x 32 19.1 us
+// wave a row, no barrier: 12288 float32 rows of 768 take 21.1 us forward and 29.4
+// backward, with four waves 23.0 and 33.4 at the best (64 rows: 3.5 and 3.2
+// forward).  Beyond, 8 to 32 features a lane (float32 rows forward with a float32
+// residual operand):
+//   2048 (4608 float32 rows)  4 x 8 features 21.9, 8 x 4 23.5, 1 x 32 21.8 us
 //                             forward, which one wave loses with few rows (64:
 //                             3.6, 3.5 and 4.6 us)
-//   4096 (2048 bf16 rows)     4 x 16 11.2, 8 x 8 12.6 us forward; backward, where
+//   4096 (2048 bf16 rows)     4 x 16 11.2, 8 x 8 12.4 us forward; backward, where
 //                             a lane holds three rows, the other way round (2300
-//                             float32 rows: 25.2 and 23.1)
-//   8192 (1152 float32 rows)  4 x 32 20.5, 8 x 16 20.1 us forward, 40.5 and 33.4
+//                             float32 rows: 25.6 and 23.1)
+//   8192 (1152 float32 rows)  4 x 32 23.2, 8 x 16 22.5 us forward, 40 and 35
 //                             backward
-//   16384 (576 float32 rows)  8 x 32 23.8, 16 x 16 23.5 us forward, 55 and 123
+//   16384 (576 float32 rows)  8 x 32 26.5, 16 x 16 26.2 us forward, 55 and 123
 //                             backward (a wave of 16 has registers for half a row)
 #define AA_NORM_SPLIT(d, CALL, SPLIT4096) \
   do {                                    \

@@ -13,11 +13,11 @@ constexpr int64_t kMaxGridThreads = (int64_t(1) << 32) - 1;
 constexpr int kTurnTokens = 64, kTurnThreads = 256;
 inline int64_t append_turn_workgroups(int64_t n) { return (n + kTurnTokens - 1) / kTurnTokens; }
 
-// Whether n tokens are turned.  From about 8 D tokens on the turning repays its
-// waits: with 8 heads of 128 and pages of 64, 512, 1024, 4096 and 40000 tokens of
-// a prompt take 5.6, 8.7, 26 and 524 us one by one and 7.3, 7.7, 10.3 and 96
-// turned; with 32 heads of 24, 128, 256 and 1024 take 3.3, 4.1, 8.4 and 3.9, 3.9,
-// 4.6.  Calls of more threads than a grid holds go one by one.
+// Whether n tokens are turned.  From 8 D tokens on the turning surely repays its
+// waits: with 8 bf16 heads of 128 and pages of 64, 512, 1024, 4096 and 40000 tokens
+// of a prompt take 5.6, 8.8, 26 and 408 us one by one and 4.7, 5.0, 8.3 and 69
+// turned; with 32 float32 heads of 24, 128, 256 and 1024 take 3.3, 4.1, 9.2 and
+// 3.3, 3.4, 3.8.  Calls of more threads than a grid holds go one by one.
 inline bool append_turns(int64_t n, int head_dim) {
   return n >= 8 * int64_t(head_dim) && append_turn_workgroups(n) * kTurnThreads <= kMaxGridThreads;
 }
@@ -38,10 +38,10 @@ inline MoeRule moe_rule(bool q2xq2, int q, int64_t D, int64_t F, int top_k, int6
   const int groups = q2xq2 ? 4 : q < 2 ? q : 2;   // of a leaf, at most
   // Waves a strip: as many as repay their join.  Measured (us of the whole call)
   // with 1, 2, 4 and 8, for sums of 8 steps of 32 rows (q = 16, 2048 -> 768) at 384
-  // strips 14.0, 13.2, 12.8, 14.1; at 768 15.5, 14.9, 15.5, 16.7; at 1536 17.2, 17.8,
-  // 17.9, 23.0.  For 16 and more steps (Q2 x Q2, 768 -> 2048) at 256 strips 19.1,
-  // 16.0, 14.8, 13.9; at 1280 20.6, 19.7, 18.8, 20.8; at 5120 44.3, 41.7, 47.6, 59.4;
-  // at 10240 48.3, 53.0, 64.8, 90.1.
+  // strips 13.5, 12.5, 12.2, 13.2; at 768 14.3, 13.7, 14.7, 15.6; at 1536 16.2, 16.5,
+  // 17.2, 22.3.  For 16 and more steps (Q2 x Q2, 768 -> 2048) at 256 strips 18.5,
+  // 15.5, 14.4, 13.4; at 1280 20.8, 19.9, 18.6, 20.9; at 5120 36.0, 33.3, 39.1, 51.1;
+  // at 10240 47.5, 52.4, 64.4, 89.8.
   const bool long_sums = groups * (D / q) >= 16 * 32;
   const uint64_t all_strips = pairs * strips;
   r.up_waves = long_sums && all_strips <= 256 ? 8 : all_strips <= (long_sums ? 1536 : 512) ? 4
@@ -51,12 +51,12 @@ inline MoeRule moe_rule(bool q2xq2, int q, int64_t D, int64_t F, int top_k, int6
   // Two strips a workgroup, which share the hidden activation's loads, where there
   // are enough of them, else one, with four or, for long sums, sixteen waves:
   // (2 strips x 8 waves, 1 x 4, 1 x 16) take for 1, 5, 10 and 20 tokens of Q2 x Q2
-  // experts (48, 240, 480, 960 strips, 128 steps) 15.9, 16.2, 14.3; 20.9, 20.7, 18.7;
-  // 24.9, 26.7, 27.2; 33.2, 35.9, 42.1 us; for 2 and 16 tokens of q = 16, 2048 -> 768
-  // (256, 2048 strips, 32 steps) 14.8, 14.6, 16.2 and 32.1, 33.5, 60.5.  Short sums
-  // of very many strips do with four waves: 32 tokens (4096 strips) 51.9 and 53.0.
-  // Workgroups of 16 waves are one a unit, so more than 256 of them take two turns:
-  // q = 2, 640 -> 1440, 7 tokens (280 strips, 276 steps) 42 us, 2 x 8 37.
+  // experts (48, 240, 480, 960 strips, 128 steps) 14.9, 15.3, 13.4; 20.7, 20.5, 18.6;
+  // 24.7, 26.5, 27.4; 33.3, 35.8, 41.7 us; for 2 and 16 tokens of q = 16, 2048 -> 768
+  // (256, 2048 strips, 32 steps) 14.0, 13.9, 15.5 and 31.2, 32.4, 59.5.  Short sums
+  // of very many strips do with four waves: 32 tokens (4096 strips) 50.8 and 52.3.
+  // Workgroups of 16 waves are one on each of the 256 units, so more of them take
+  // two turns: q = 2, 640 -> 1440, 7 tokens (280 strips, 276 steps) 39.8 us, 2 x 8 35.1.
   const int64_t steps = top_k * int64_t(groups) * ((F / q + 31) / 32);
   const uint64_t all_out = uint64_t(M) * uint64_t(D / 16);
   if (all_out >= 1536 && steps <= 64) r.down_strips = 2, r.down_waves = 4;
